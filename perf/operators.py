@@ -12,7 +12,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-MIN_EXP, MAX_EXP = -120, 120  # range of a cache page's scale exponent
+MIN_EXP, MAX_EXP = -120, 119  # range of a cache page's scale exponent
 
 
 # ------------------------------------------------------------------ the cases
