@@ -12,9 +12,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libac.so")
 
 AC_OK, AC_ERR_INVALID_ARG, AC_ERR_UNSUPPORTED, AC_ERR_WORKSPACE, AC_ERR_CUDA, \
-    AC_ERR_NONFINITE, AC_ERR_TIMEOUT, AC_ERR_STATE = range(8)
+    AC_ERR_NONFINITE, AC_ERR_TIMEOUT, AC_ERR_STATE, AC_ERR_BOUNDS = range(9)
 STATUS_NAMES = ["AC_OK", "AC_ERR_INVALID_ARG", "AC_ERR_UNSUPPORTED", "AC_ERR_WORKSPACE", "AC_ERR_CUDA",
-                "AC_ERR_NONFINITE", "AC_ERR_TIMEOUT", "AC_ERR_STATE"]
+                "AC_ERR_NONFINITE", "AC_ERR_TIMEOUT", "AC_ERR_STATE", "AC_ERR_BOUNDS"]
 
 AC_TAU_ABSOLUTE, AC_TAU_MEAN_FACTOR, AC_TAU_PERCENTILE = 0, 1, 2
 
@@ -76,11 +76,31 @@ class ACAssignCounters(ctypes.Structure):
                 ("full_rescore_rows", ctypes.c_int64)]
 
 
+class ACView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_l", ctypes.c_int64)]
+
+
+class ACWindow(ctypes.Structure):
+    _fields_ = [("left", ctypes.c_int32), ("right", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class ACCache8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+AC_DTYPE_BF16, AC_DTYPE_F16, AC_DTYPE_F32 = range(3)
+
 # every function that include/ac.h declares, with its ctypes signature
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 # int32_t (*ac_sum_u64_fn)(void *user, uint64_t *data, int32_t count)
 SUM_U64_FN = ctypes.CFUNCTYPE(ctypes.c_int32, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint64), ctypes.c_int32)
+_VW, _WN, _C8 = ctypes.POINTER(ACView), ctypes.POINTER(ACWindow), ctypes.POINTER(ACCache8)
+_I64P = ctypes.POINTER(ctypes.c_int64)
 SIGNATURES = {
     "ac_create": (_I, [ctypes.POINTER(ACConfig), _I, _I, _I, _I, ctypes.POINTER(_P)]),
     "ac_destroy": (_I, [_P]),
@@ -106,6 +126,16 @@ SIGNATURES = {
     "ac_tau_mean_from_sums": (_I, [ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_float)]),
     "ac_tau_radix_pick": (_I, [ctypes.POINTER(ctypes.c_uint64), _I, ctypes.POINTER(ctypes.c_uint32)]),
     "ac_state_import": (_I, [_P, _P, ctypes.c_int64]),
+    "ac_rope_axes": (_I, [_I, _VW, _VW, _I, _VW, _VW, _I, _I, _I, _I, _P, ctypes.c_int64,
+                          ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I), _I, _I, _I, _P]),
+    "ac_window_attn_workspace": (_I, [_I] * 6 + [_WN, _I64P]),
+    "ac_window_attn": (_I, [_VW] * 4 + [_P] + [_I] * 6 + [_P, _P, _WN, _P, ctypes.c_int64, _P]),
+    "ac_window_attn_backward_workspace": (_I, [_I] * 6 + [_I64P]),
+    "ac_window_attn_backward": (_I, [_VW] * 5 + [_P] + [_VW] * 3 + [_I] * 6 + [_P, _P, _WN, _P, ctypes.c_int64, _P]),
+    "ac_cache8_append": (_I, [_C8, _VW, _VW, _I, _I, _P, _I, _P, _P, _P]),
+    "ac_cache8_attn_workspace": (_I, [_C8, _I, _I, _I, _I, _WN, _I64P]),
+    "ac_cache8_attn": (_I, [_C8, _VW, _VW, _P, _I, _I, _I, _P, _I, _P, _P, _WN, _P, ctypes.c_int64, _P]),
+    "ac_ops_status": (_I, [_P]),
 }
 
 _lib = None

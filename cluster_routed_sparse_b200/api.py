@@ -165,7 +165,12 @@ class SparseLayer:
               self.ctx)
         return O
 
-    def forward(self, Q, K, V, O=None, warm: bool = False, times: bool = False):
+    def forward(self, Q, K, V, O=None, warm: bool = False, times: bool = False, rope=None):
+        """rope: (positions, pairs) or (positions, pairs, theta) of streaming.rope_axes:
+        Q and K are rotated first (into new tensors; any strides then)."""
+        if rope is not None:
+            from .streaming import rope_axes
+            Q, K = rope_axes(Q, K, *rope)
         if O is None:
             O = torch.empty_like(Q)
         t = ACStageTimes() if times else None

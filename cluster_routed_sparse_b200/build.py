@@ -14,8 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libac.so")
 SOURCES = ["ac_api.cu", "cluster_kernels.cu", "assign_mma.cu", "score_kernels.cu", "quest_mma.cu", "attn_kernel.cu",
-           "noalloc.cu"]
-HEADERS = ["ac_device.cuh", "ac_internal.h"]
+           "noalloc.cu", "stream_api.cu", "rope_axes.cu", "cache8.cu", "window_simple.cu"]
+HEADERS = ["ac_device.cuh", "ac_internal.h", "stream_device.cuh", "stream_internal.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -39,7 +39,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile every CUDA source into one shared library next to this file."""
     if not force and not _stale():
         return LIB
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
            "-o", LIB + ".tmp"] + [os.path.join(CSRC, f) for f in SOURCES] + ["-lcudart"]
     if ptxas_verbose:

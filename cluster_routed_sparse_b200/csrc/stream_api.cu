@@ -1,0 +1,296 @@
+// stream_api.cu -- C ABI of the streaming operators: checks of arguments,
+// argument blocks and the error words.
+#include <cmath>
+#include <cstdio>
+
+#include "stream_device.cuh"
+
+using namespace ac;
+
+namespace {
+
+__device__ OpErr g_op_err;
+std::atomic<uint32_t> g_launch_id{0};
+
+ac_status refuse(const char *what, ac_status st = AC_ERR_INVALID_ARG) {
+    set_static_error(what);
+    return st;
+}
+
+ac_status cuda_refuse(const char *fn, cudaError_t e) {
+    char buf[256];
+    snprintf(buf, sizeof(buf), "%s: %s", fn, cudaGetErrorString(e));
+    set_static_error(buf);
+    return AC_ERR_CUDA;
+}
+
+// The kernels are built for sm_100a only.
+ac_status check_device(const char *fn) {
+    int dev = 0, major = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e != cudaSuccess) return cuda_refuse(fn, e);
+    if (major != 10) return refuse("the streaming operators need an sm_100 device", AC_ERR_UNSUPPORTED);
+    return AC_OK;
+}
+
+constexpr int kMaxLen = 1 << 30;
+
+View view_of(const ac_view *v) { return View{v->data, v->stride_b, v->stride_h, v->stride_l}; }
+
+// 16-byte rows: what the vector and bulk tensor loads need.  A stride of a
+// dimension of one entry is never used.
+bool rows16(const ac_view *v, int B, int H, int L) {
+    if (!v || !v->data || (reinterpret_cast<uintptr_t>(v->data) & 15u)) return false;
+    const int64_t st[3] = {v->stride_b, v->stride_h, v->stride_l};
+    const int n[3] = {B, H, L};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] <= 0 || st[i] % 8 || st[i] >= (int64_t(1) << 38))) return false;
+    return true;
+}
+
+ac_status window_rule(const ac_window *w, int d, WinRule *out, float *scale) {
+    if (!w || w->left < -1 || w->right < -1 || w->sinks < 0 || w->block < 1 || !std::isfinite(w->scale))
+        return refuse("window: left and right must be >= -1, sinks >= 0, block >= 1 and the scale finite");
+    *out = WinRule{w->left, w->right, w->sinks, w->block};
+    *scale = w->scale != 0.f ? w->scale : 1.f / sqrtf((float)d);
+    return AC_OK;
+}
+
+ac_status check_sizes(int B, int Hq, int Hk, int Lq, int Lk, int d) {
+    if (d != 64 && d != 128) return refuse("window attention: d must be 64 or 128", AC_ERR_UNSUPPORTED);
+    if (B < 0 || Hq < 1 || Hk < 1 || Lq < 0 || Lk < 0 || Lq > kMaxLen || Lk > kMaxLen)
+        return refuse("window attention: bad sizes");
+    if (Hq % Hk || Hq / Hk > 128)
+        return refuse("window attention: query heads must be a multiple of the key heads, at most 128 for each");
+    const int64_t rows = (int64_t)B * Hq * (int64_t)std::max(Lq, 1), keys = (int64_t)B * Hk * (int64_t)std::max(Lk, 1);
+    if (B > 65535 || Hq > 65535 || rows > (int64_t(1) << 32) || keys > (int64_t(1) << 32))
+        return refuse("window attention: at most 2^32 rows of queries and of keys");
+    return AC_OK;
+}
+
+}  // namespace
+
+cudaError_t ac::op_err_address(OpErr **out) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_op_err);
+}
+
+uint32_t ac::next_launch_id() {
+    uint32_t id;
+    do id = g_launch_id.fetch_add(1, std::memory_order_relaxed) + 1;
+    while (id == 0);
+    return id;
+}
+
+extern "C" ac_status ac_ops_status(void *stream) {
+    OpErr *p = nullptr, h;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = op_err_address(&p);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&h, p, sizeof(h), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_refuse("ac_ops_status", e);
+    if (h.timeout || h.bits) {
+        e = cudaMemsetAsync(p, 0, sizeof(h), s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e != cudaSuccess) return cuda_refuse("ac_ops_status", e);
+    }
+    if (h.timeout || (h.bits & DEV_ERR_TIMEOUT)) return refuse("a bounded in-kernel wait expired", AC_ERR_TIMEOUT);
+    if (h.bits) return refuse("a length or a page index on the device is out of range", AC_ERR_BOUNDS);
+    return AC_OK;
+}
+
+extern "C" ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view *y, int32_t H, const ac_view *x2,
+                                  const ac_view *y2, int32_t H2, int32_t B, int32_t L, int32_t d,
+                                  const int32_t *positions, int64_t pos_stride_b, const double *freq,
+                                  const int32_t *pairs, int32_t n_axes, int32_t interleaved, int32_t inverse,
+                                  void *stream) {
+    if (dtype < AC_DTYPE_BF16 || dtype > AC_DTYPE_F32) return refuse("ac_rope_axes: unknown dtype", AC_ERR_UNSUPPORTED);
+    if (d < 2 || d > 256 || d % 2) return refuse("ac_rope_axes: d must be even and at most 256", AC_ERR_UNSUPPORTED);
+    if (!freq || !pairs || n_axes < 1 || n_axes > 8 || B < 0 || L < 0 || H < 0 || H2 < 0 || H > 65535 || H2 > 65535)
+        return refuse("ac_rope_axes: invalid argument");
+    RopeArgs a;
+    a.P = 0;
+    for (int i = 0; i < n_axes; ++i) {
+        if (pairs[i] < 0 || pairs[i] > d / 2 - a.P) return refuse("ac_rope_axes: the axes' pairs must fit in d / 2");
+        for (int k = 0; k < pairs[i]; ++k) {
+            const double f = freq[a.P];
+            if (!std::isfinite(f)) return refuse("ac_rope_axes: frequencies must be finite");
+            const long double two_pi = 6.283185307179586476925286766559L;
+            long double t = fmodl((long double)f / two_pi, 1.0L);
+            if (t < 0) t += 1.0L;
+            const long double scaled = roundl(t * 18446744073709551616.0L);
+            a.turns[a.P] = scaled >= 18446744073709551616.0L ? 0 : (uint64_t)scaled;
+            a.axis[a.P] = (uint8_t)i;
+            ++a.P;
+        }
+    }
+    if (B == 0 || L == 0 || H + H2 == 0) return AC_OK;
+    if (!positions || (H && (!x || !y || !x->data || !y->data)) || (H2 && (!x2 || !y2 || !x2->data || !y2->data)))
+        return refuse("ac_rope_axes: NULL tensor");
+    a.H[0] = H, a.H[1] = H2;
+    for (int t = 0; t < 2; ++t) {
+        const ac_view *in = t ? x2 : x, *out = t ? y2 : y;
+        a.x[t] = a.H[t] ? view_of(in) : View{};
+        a.y[t] = a.H[t] ? view_of(out) : View{};
+    }
+    a.B = B, a.L = L, a.d = d;
+    a.pos = positions, a.pos_b = pos_stride_b, a.n_axes = n_axes;
+    a.interleaved = interleaved != 0, a.inverse = inverse != 0;
+    const ac_status st = check_device("ac_rope_axes");
+    if (st != AC_OK) return st;
+    const cudaError_t e = launch_rope(dtype, a, (cudaStream_t)stream);
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_rope_axes", e);
+}
+
+// ---------------------------------------------------------------- window attention
+extern "C" ac_status ac_window_attn_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk, int32_t d,
+                                              const ac_window *w, int64_t *bytes) {
+    if (!bytes) return refuse("ac_window_attn_workspace: NULL argument");
+    ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
+    WinRule r;
+    float scale;
+    if (st == AC_OK) st = window_rule(w, d, &r, &scale);
+    if (st != AC_OK) return st;
+    *bytes = 0;
+    return AC_OK;
+}
+
+extern "C" ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac_view *v, const ac_view *o, float *lse,
+                                    int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk, int32_t d,
+                                    const int32_t *q_lens, const int32_t *k_lens, const ac_window *w, void *workspace,
+                                    int64_t workspace_bytes, void *stream) {
+    ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
+    WinArgs a{};
+    if (st == AC_OK) st = window_rule(w, d, &a.w, &a.scale);
+    int64_t need = 0;
+    if (st == AC_OK) st = ac_window_attn_workspace(B, Hq, Hk, Lq, Lk, d, w, &need);
+    if (st != AC_OK) return st;
+    if (B == 0 || Lq == 0) return AC_OK;
+    if (!rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq) || (Lk > 0 && (!rows16(k, B, Hk, Lk) || !rows16(v, B, Hk, Lk))))
+        return refuse("ac_window_attn: tensors must be 16-byte aligned with positive strides in multiples of 8");
+    if (workspace_bytes < need || (need && !workspace))
+        return refuse("ac_window_attn: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_device("ac_window_attn")) != AC_OK) return st;
+    a.q = view_of(q), a.o = view_of(o);
+    if (Lk > 0) a.k = view_of(k), a.v = view_of(v);
+    a.lse = lse, a.q_lens = q_lens, a.k_lens = k_lens;
+    a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
+    a.ws = workspace;
+    cudaError_t e = op_err_address(&a.err);
+    if (e == cudaSuccess) e = launch_window_simple(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_window_attn", e);
+}
+
+extern "C" ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
+                                                       int32_t d, int64_t *bytes) {
+    if (!bytes) return refuse("ac_window_attn_backward_workspace: NULL argument");
+    const ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
+    if (st != AC_OK) return st;
+    *bytes = 0;
+    return AC_OK;
+}
+
+extern "C" ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *q, const ac_view *k, const ac_view *v,
+                                             const ac_view *o, const float *lse, const ac_view *dq, const ac_view *dk,
+                                             const ac_view *dv, int32_t B, int32_t Hq, int32_t Hk, int32_t Lq,
+                                             int32_t Lk, int32_t d, const int32_t *q_lens, const int32_t *k_lens,
+                                             const ac_window *w, void *workspace, int64_t workspace_bytes,
+                                             void *stream) {
+    ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
+    WinBwdArgs g{};
+    WinArgs &a = g.f;
+    if (st == AC_OK) st = window_rule(w, d, &a.w, &a.scale);
+    int64_t need = 0;
+    if (st == AC_OK) st = ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, &need);
+    if (st != AC_OK) return st;
+    if (B == 0 || (Lq == 0 && Lk == 0)) return AC_OK;
+    if ((Lq > 0 && (!lse || !rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq) || !rows16(d_o, B, Hq, Lq) ||
+                    !rows16(dq, B, Hq, Lq))) ||
+        (Lk > 0 && (!rows16(k, B, Hk, Lk) || !rows16(v, B, Hk, Lk) || !rows16(dk, B, Hk, Lk) || !rows16(dv, B, Hk, Lk))))
+        return refuse("ac_window_attn_backward: tensors must be 16-byte aligned with positive strides in multiples of 8");
+    if (workspace_bytes < need || (need && !workspace))
+        return refuse("ac_window_attn_backward: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_device("ac_window_attn_backward")) != AC_OK) return st;
+    if (Lq > 0) a.q = view_of(q), a.o = view_of(o), g.go = view_of(d_o), g.dq = view_of(dq);
+    if (Lk > 0) a.k = view_of(k), a.v = view_of(v), g.dk = view_of(dk), g.dv = view_of(dv);
+    a.lse = const_cast<float *>(lse), a.q_lens = q_lens, a.k_lens = k_lens;
+    a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
+    a.ws = workspace;
+    cudaError_t e = op_err_address(&a.err);
+    if (e == cudaSuccess) e = launch_window_bwd_simple(g, (cudaStream_t)stream);
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_window_attn_backward", e);
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+namespace {
+ac_status check_cache(const ac_cache8 *c, int max_pages) {
+    if (!c || c->pages < 0 || c->heads < 1 || max_pages < 0) return refuse("8-bit cache: invalid argument");
+    if (c->d != 64 && c->d != 128) return refuse("8-bit cache: d must be 64 or 128", AC_ERR_UNSUPPORTED);
+    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+        return refuse("8-bit cache: pages must hold 16, 32, 64 or 128 tokens", AC_ERR_UNSUPPORTED);
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || (reinterpret_cast<uintptr_t>(c->k) & 15u) ||
+        (reinterpret_cast<uintptr_t>(c->v) & 15u))
+        return refuse("8-bit cache: codes must be 16-byte aligned");
+    if ((int64_t)max_pages * c->page_tokens > kMaxLen) return refuse("8-bit cache: sequences of at most 2^30 tokens");
+    return AC_OK;
+}
+}  // namespace
+
+extern "C" ac_status ac_cache8_append(const ac_cache8 *cache, const ac_view *k, const ac_view *v, int32_t B, int32_t n,
+                                      const int32_t *page_table, int32_t max_pages, const int32_t *start,
+                                      const int32_t *counts, void *stream) {
+    ac_status st = check_cache(cache, max_pages);
+    if (st != AC_OK) return st;
+    if (B < 0 || n < 0 || n > kMaxLen) return refuse("ac_cache8_append: bad sizes");
+    if (B == 0 || n == 0) return AC_OK;
+    if (!page_table || !start) return refuse("ac_cache8_append: NULL page table or lengths");
+    if (!rows16(k, B, cache->heads, n) || !rows16(v, B, cache->heads, n))
+        return refuse("ac_cache8_append: tensors must be 16-byte aligned with positive strides in multiples of 8");
+    if ((st = check_device("ac_cache8_append")) != AC_OK) return st;
+    AppendArgs a{cache->k, cache->v, cache->k_scale, cache->v_scale, view_of(k), view_of(v), page_table, start, counts,
+                 cache->pages, cache->heads, cache->page_tokens, cache->d, B, n, max_pages, nullptr};
+    cudaError_t e = op_err_address(&a.err);
+    if (e == cudaSuccess) e = launch_cache8_append(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_cache8_append", e);
+}
+
+extern "C" ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B, int32_t Hq, int32_t Lq,
+                                              int32_t max_pages, const ac_window *w, int64_t *bytes) {
+    if (!bytes) return refuse("ac_cache8_attn_workspace: NULL argument");
+    ac_status st = check_cache(cache, max_pages);
+    if (st == AC_OK) st = check_sizes(B, Hq, cache->heads, Lq, max_pages * cache->page_tokens, cache->d);
+    WinRule r;
+    float scale;
+    if (st == AC_OK) st = window_rule(w, cache->d, &r, &scale);
+    if (st != AC_OK) return st;
+    *bytes = 0;
+    return AC_OK;
+}
+
+extern "C" ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, const ac_view *o, float *lse, int32_t B,
+                                    int32_t Hq, int32_t Lq, const int32_t *page_table, int32_t max_pages,
+                                    const int32_t *q_lens, const int32_t *k_lens, const ac_window *w, void *workspace,
+                                    int64_t workspace_bytes, void *stream) {
+    int64_t need = 0;
+    ac_status st = ac_cache8_attn_workspace(cache, B, Hq, Lq, max_pages, w, &need);
+    if (st != AC_OK) return st;
+    if (B == 0 || Lq == 0) return AC_OK;
+    if (!k_lens || (max_pages > 0 && !page_table)) return refuse("ac_cache8_attn: NULL page table or lengths");
+    if (!rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq))
+        return refuse("ac_cache8_attn: tensors must be 16-byte aligned with positive strides in multiples of 8");
+    if (workspace_bytes < need || (need && !workspace))
+        return refuse("ac_cache8_attn: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_device("ac_cache8_attn")) != AC_OK) return st;
+    WinArgs a{};
+    if ((st = window_rule(w, cache->d, &a.w, &a.scale)) != AC_OK) return st;
+    a.q = view_of(q), a.o = view_of(o);
+    a.k8 = cache->k, a.v8 = cache->v, a.ks = cache->k_scale, a.vs = cache->v_scale;
+    a.table = page_table, a.pages = cache->pages, a.T = cache->page_tokens, a.max_pages = max_pages;
+    a.lse = lse, a.q_lens = q_lens, a.k_lens = k_lens;
+    a.B = B, a.Hq = Hq, a.Hk = cache->heads, a.G = Hq / cache->heads, a.Lq = Lq;
+    a.Lk = max_pages * cache->page_tokens, a.d = cache->d;
+    a.ws = workspace;
+    cudaError_t e = op_err_address(&a.err);
+    if (e == cudaSuccess) e = launch_window_simple(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_cache8_attn", e);
+}

@@ -1,0 +1,284 @@
+"""Streaming operators over torch tensors: what surrounds the attention of a
+video generator that works frame after frame.
+
+    rope_axes               rotary embedding over several axes, and its inverse
+    window_attn             attention within a window and over a few first tokens
+    window_attn_backward    its gradients
+    Cache8, cache8_append, cache8_attn
+                            a paged cache of keys and values in 8 bits, and the
+                            attention that reads it
+    ops_status              waits, and raises what the kernels have noted
+
+Each call forwards data pointers, strides and the current stream of the
+tensors' device to the C ABI in include/ac.h, which documents the operators;
+all arithmetic runs in libac's kernels.  Tensors are [B, H, L, d] in any strides
+(d contiguous).  Nothing here synchronises but ops_status.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from ._lib import ACCache8, ACView, ACWindow, check
+
+_ROPE_DTYPES = {torch.bfloat16: _lib.AC_DTYPE_BF16, torch.float16: _lib.AC_DTYPE_F16, torch.float32: _lib.AC_DTYPE_F32}
+_NO_VIEW = ACView(None, 0, 0, 0)
+
+
+def _on(device, fn, *args):
+    """fn(*args, stream) with `device` current."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _view(t, name, device, shape=None, dtype=torch.bfloat16):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be [B, H, L, d]" + (f" = {shape}" if shape else "") + f", got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    b, h, row, e = t.stride()
+    if e != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return ACView(t.data_ptr(), b, h, row)
+
+
+def _ints(t, name, device, shape):
+    """Pointer of a contiguous int32 tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------- rotary embedding
+@functools.lru_cache(maxsize=64)
+def _axes(pairs, theta):
+    """Frequencies of the pairs: axis i has the series theta^(-k / pairs[i]) of its own."""
+    theta = (theta,) * len(pairs) if not isinstance(theta, tuple) else theta
+    if len(theta) != len(pairs) or any(n < 0 for n in pairs) or any(not t > 0 for t in theta):
+        raise ValueError("one theta > 0 for all axes, or one for each; pairs >= 0")
+    freq = [t ** (-k / n) for n, t in zip(pairs, theta) for k in range(n)]
+    return (ctypes.c_double * max(1, len(freq)))(*freq), (ctypes.c_int32 * max(1, len(pairs)))(*pairs)
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_given(pairs, freqs):
+    if len(freqs) != sum(pairs):
+        raise ValueError("one frequency for each pair")
+    return (ctypes.c_double * max(1, len(freqs)))(*freqs), (ctypes.c_int32 * max(1, len(pairs)))(*pairs)
+
+
+def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved: bool = True, inverse: bool = False,
+              out=None):
+    """Rotate q [B, Hq, L, d] and k [B, Hk, L, d] (k may be None) by their tokens'
+    positions along several axes (ac_rope_axes).
+
+    positions: int32 [L, axes] or [B, L, axes]; pairs: how many of the d / 2
+    element pairs turn with each axis, in order (what is left stays as it is);
+    theta: base of the frequencies, one or one for each axis, or freqs: radians
+    per step of each pair.  interleaved: pairs (2p, 2p + 1), otherwise
+    (p, P + p).  inverse=True rotates back: the gradient with respect to the
+    input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
+    the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
+    fp32.  Returns (q, k) rotated, or q alone when k is None."""
+    dtype = _ROPE_DTYPES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("q must be bf16, fp16 or fp32")
+    dev = q.device
+    vq = _view(q, "q", dev, None, q.dtype)
+    B, Hq, L, d = q.shape
+    pairs = tuple(pairs)
+    if freqs is not None:
+        freq, npairs = _axes_given(pairs, tuple(freqs))
+    else:
+        freq, npairs = _axes(pairs, theta if not isinstance(theta, (list, tuple)) else tuple(theta))
+    axes = len(pairs)
+    if positions.dim() == 3:
+        pos, pos_b = _ints(positions, "positions", dev, (B, L, axes)), L * axes
+    else:
+        pos, pos_b = _ints(positions, "positions", dev, (L, axes)), 0
+    Hk = 0
+    vk = vko = _NO_VIEW
+    oq, ok = out if out is not None else (None, None)
+    if oq is None:
+        oq = torch.empty((B, Hq, L, d), dtype=q.dtype, device=dev)
+    vqo = _view(oq, "out[0]", dev, (B, Hq, L, d), q.dtype)
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 4 else 0
+        vk = _view(k, "k", dev, (B, Hk, L, d), q.dtype)
+        if ok is None:
+            ok = torch.empty((B, Hk, L, d), dtype=q.dtype, device=dev)
+        vko = _view(ok, "out[1]", dev, (B, Hk, L, d), q.dtype)
+    _on(dev, _lib.load().ac_rope_axes, dtype, vq, vqo, Hq, vk, vko, Hk, B, L, d, pos, pos_b, freq, npairs, axes,
+        int(interleaved), int(inverse))
+    return oq if k is None else (oq, ok)
+
+
+# ---------------------------------------------------------------- window attention
+@functools.lru_cache(maxsize=256)
+def _window(left, right, sinks, block, scale):
+    return ACWindow(left, right, sinks, block, scale)
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block):
+    n = ctypes.c_int64(0)
+    check(_lib.load().ac_window_attn_workspace(B, Hq, Hk, Lq, Lk, d, _window(left, right, sinks, block, 0.0),
+                                               ctypes.byref(n)))
+    return n.value
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1, q_lens=None, k_lens=None,
+                scale: float = 0.0, out=None, return_lse: bool = False):
+    """Softmax attention of q [B, Hq, Lq, d] over k, v [B, Hk, Lk, d] (bf16) within a
+    window of `left` blocks back and `right` ahead (-1: no bound), blocks of
+    `block` tokens, plus the first `sinks` tokens (ac_window_attn; struct
+    ac_window says exactly which keys a query sees).  q_lens, k_lens: int32 [B]
+    lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32."""
+    dev = q.device
+    vq = _view(q, "q", dev)
+    B, Hq, Lq, d = q.shape
+    Hk, Lk = (k.shape[1], k.shape[2]) if k.dim() == 4 else (0, 0)
+    vk, vv = _view(k, "k", dev, (B, Hk, Lk, d)), _view(v, "v", dev, (B, Hk, Lk, d))
+    if out is None:
+        out = torch.empty((B, Hq, Lq, d), dtype=torch.bfloat16, device=dev)
+    vo = _view(out, "out", dev, (B, Hq, Lq, d))
+    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev) if return_lse else None
+    n = _window_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block)
+    ws = _workspace(n, dev)
+    _on(dev, _lib.load().ac_window_attn, vq, vk, vv, vo, _ptr(lse), B, Hq, Hk, Lq, Lk, d,
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)),
+        _window(left, right, sinks, block, scale), _ptr(ws), n)
+    return (out, lse) if return_lse else out
+
+
+def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1,
+                         q_lens=None, k_lens=None, scale: float = 0.0, out=None):
+    """Gradients (dq, dk, dv) of window_attn with the same window and lengths, from
+    d_out, the gradient of o, and the o and lse that it returned
+    (ac_window_attn_backward).  out: (dq, dk, dv) to write into."""
+    dev = q.device
+    vq = _view(q, "q", dev)
+    B, Hq, Lq, d = q.shape
+    Hk, Lk = (k.shape[1], k.shape[2]) if k.dim() == 4 else (0, 0)
+    qs, ks = (B, Hq, Lq, d), (B, Hk, Lk, d)
+    vk, vv = _view(k, "k", dev, ks), _view(v, "v", dev, ks)
+    vo, vg = _view(o, "o", dev, qs), _view(d_out, "d_out", dev, qs)
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Lq) or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError(f"lse must be a contiguous fp32 tensor {(B, Hq, Lq)} on {dev}")
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in (qs, ks, ks))
+    dq, dk, dv = out
+    n = ctypes.c_int64(0)
+    lib = _lib.load()
+    check(lib.ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, ctypes.byref(n)))
+    ws = _workspace(n.value, dev)
+    _on(dev, lib.ac_window_attn_backward, vg, vq, vk, vv, vo, lse.data_ptr(), _view(dq, "dq", dev, qs),
+        _view(dk, "dk", dev, ks), _view(dv, "dv", dev, ks), B, Hq, Hk, Lq, Lk, d,
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)),
+        _window(left, right, sinks, block, scale), _ptr(ws), n.value)
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------- 8-bit cache
+class Cache8(NamedTuple):
+    """The tensors of a paged 8-bit cache: k, v float8_e4m3fn [pages, heads, page_tokens, d]
+    and k_scale, v_scale fp32 [pages, heads], powers of two (struct ac_cache8)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_tokens: int, d: int, device="cuda"):
+        """A cache that holds zeros."""
+        k, v = (torch.zeros((pages, heads, page_tokens, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                for _ in range(2))
+        ks, vs = (torch.full((pages, heads), 2.0 ** -120, dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _cache(c, dev):
+    pages, heads, T, d = c.k.shape
+    for t, n in ((c.k, "k"), (c.v, "v")):
+        if t.dtype != torch.float8_e4m3fn or tuple(t.shape) != (pages, heads, T, d) or not t.is_contiguous() \
+                or t.device != dev:
+            raise ValueError(f"cache.{n} must be a contiguous float8_e4m3fn tensor [pages, heads, page_tokens, d] on {dev}")
+    for t, n in ((c.k_scale, "k_scale"), (c.v_scale, "v_scale")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (pages, heads) or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"cache.{n} must be a contiguous fp32 tensor [pages, heads] on {dev}")
+    return ACCache8(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), pages, heads, T, d)
+
+
+def cache8_append(k, v, cache: Cache8, page_table, start, counts=None):
+    """Write the new tokens k, v [B, heads, n, d] (bf16) of each sequence behind its
+    first start[b] tokens into the cache (ac_cache8_append).  page_table: int32
+    [B, max_pages]; start, counts: int32 [B] (counts: how many of the n are real)."""
+    dev = k.device
+    vk = _view(k, "k", dev)
+    B, H, n, d = k.shape
+    vv = _view(v, "v", dev, (B, H, n, d))
+    c = _cache(cache, dev)
+    if (H, d) != (c.heads, c.d):
+        raise ValueError(f"k has {H} heads of {d}, the cache {c.heads} of {c.d}")
+    if start is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages] and start [B]")
+    _on(dev, _lib.load().ac_cache8_append, c, vk, vv, B, n,
+        _ints(page_table, "page_table", dev, (B, page_table.shape[1])), page_table.shape[1],
+        _ints(start, "start", dev, (B,)), _ints(counts, "counts", dev, (B,)))
+
+
+def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1,
+                q_lens=None, scale: float = 0.0, out=None, return_lse: bool = False):
+    """window_attn of q [B, Hq, Lq, d] over the first k_lens[b] cached tokens of each
+    sequence (ac_cache8_attn)."""
+    dev = q.device
+    vq = _view(q, "q", dev)
+    B, Hq, Lq, d = q.shape
+    c = _cache(cache, dev)
+    if d != c.d:
+        raise ValueError(f"q has heads of {d}, the cache of {c.d}")
+    if k_lens is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages] and k_lens [B]")
+    if out is None:
+        out = torch.empty((B, Hq, Lq, d), dtype=torch.bfloat16, device=dev)
+    vo = _view(out, "out", dev, (B, Hq, Lq, d))
+    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev) if return_lse else None
+    lib, w = _lib.load(), _window(left, right, sinks, block, scale)
+    n = ctypes.c_int64(0)
+    check(lib.ac_cache8_attn_workspace(c, B, Hq, Lq, page_table.shape[1], w, ctypes.byref(n)))
+    ws = _workspace(n.value, dev)
+    _on(dev, lib.ac_cache8_attn, c, vq, vo, _ptr(lse), B, Hq, Lq,
+        _ints(page_table, "page_table", dev, (B, page_table.shape[1])), page_table.shape[1],
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n.value)
+    return (out, lse) if return_lse else out
+
+
+def ops_status(device=None):
+    """Wait for the current stream of `device` and raise ACError for what kernels of
+    these operators have noted there since the last call: a length or page index
+    out of range (AC_ERR_BOUNDS) or an expired wait (AC_ERR_TIMEOUT)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    _on(dev, _lib.load().ac_ops_status)

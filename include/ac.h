@@ -53,8 +53,9 @@ typedef enum ac_status {
     AC_ERR_CUDA = 4,         /* a CUDA runtime call failed                     */
     AC_ERR_NONFINITE = 5,    /* NaN or Inf in an input                          */
     AC_ERR_TIMEOUT = 6,      /* a bounded in-kernel wait expired                */
-    AC_ERR_STATE = 7         /* call needs state that is not there (e.g. warm
+    AC_ERR_STATE = 7,        /* call needs state that is not there (e.g. warm
                                 step before any step 0)                        */
+    AC_ERR_BOUNDS = 8        /* a length or index in device memory out of range */
 } ac_status;
 
 /* Rule for the distance threshold tau of Algorithm 1.  The pages define it as
@@ -408,6 +409,125 @@ AC_API ac_status ac_get_launch_count(int64_t *out);
  * Both synchronise the device. */
 AC_API ac_status ac_state_export(ac_ctx *ctx, void *host_buf, int64_t *bytes);
 AC_API ac_status ac_state_import(ac_ctx *ctx, const void *host_buf, int64_t bytes);
+
+/* ------------------------------------------------------------------------
+ * Streaming operators: what surrounds the attention of a video generator that
+ * works frame after frame.  They take no context: every call gets its tensors,
+ * a workspace where one is named (its size from the _workspace function, any
+ * contents, 256-byte aligned, in use until the call's work on `stream` ends),
+ * and runs on the current device, asynchronously on `stream`; all of them may
+ * be captured into a CUDA graph.  Calls on different streams, with workspaces
+ * of their own, may overlap.  Errors of arguments are returned at once
+ * (ac_last_error_string(NULL) describes them); what only the device can see
+ * (lengths, page indices, an expired wait) is clamped or left out there and
+ * reported by the next ac_ops_status on that device.
+ *
+ * ac_view: [B, H, L, d] elements, d contiguous, the other strides in elements
+ * and free; the attention and the cache take bf16 rows on 16-byte boundaries
+ * (strides in positive multiples of 8 where the dimension has more than one
+ * entry).  A stride of 0 (a broadcast tensor) is refused there.  Inputs may
+ * overlap one another; outputs overlap nothing else unless stated. */
+typedef struct ac_view {
+    void *data;
+    int64_t stride_b, stride_h, stride_l;
+} ac_view;
+
+typedef enum ac_dtype { AC_DTYPE_BF16 = 0, AC_DTYPE_F16 = 1, AC_DTYPE_F32 = 2 } ac_dtype;
+
+/* Rotary embedding over n_axes axes (time, height, width, ...), of one tensor
+ * or of queries and keys in one launch (H2 = 0: one tensor).  The first
+ * sum(pairs) pairs of a row rotate, pairs[i] of them with axis i, pair p by the
+ * angle positions[b, l, axis(p)] * freq[p] (freq: host, radians per step, one
+ * per pair, fp64); elements behind them are copied.  interleaved: pair p is
+ * elements (2p, 2p + 1); otherwise (p, P + p) with P = sum(pairs).  inverse
+ * rotates back, which is also the gradient.  positions: device int32
+ * [L, n_axes] for every sequence (pos_stride_b = 0) or per sequence
+ * (pos_stride_b = entries from one to the next).  Angles are exact to 2^-32
+ * turns at every position.  d even, at most 256; any strides.  y may be x itself.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, d, device), CUDA. */
+AC_API ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view *y, int32_t H, const ac_view *x2,
+                              const ac_view *y2, int32_t H2, int32_t B, int32_t L, int32_t d,
+                              const int32_t *positions, int64_t pos_stride_b, const double *freq,
+                              const int32_t *pairs, int32_t n_axes, int32_t interleaved, int32_t inverse,
+                              void *stream);
+
+/* Which keys a query sees.  Query i of a sequence of ql queries and kl keys
+ * stands at position i + kl - ql (the last query at the last key); with
+ * blk(x) = floor(x / block) it sees key j when j < kl, blk(j) <= blk(pos) +
+ * right, and blk(j) >= blk(pos) - left or j < sinks.  left, right = -1: no
+ * bound on that side; block = tokens per frame makes the window one of whole
+ * frames, block = 1 one of tokens.  scale: 0 selects 1/sqrt(d). */
+typedef struct ac_window {
+    int32_t left, right, sinks, block;
+    float scale;
+} ac_window;
+
+/* Softmax attention over the visible keys.  q, o: [B, Hq, Lq, d]; k, v:
+ * [B, Hk, Lk, d], Hq a multiple of Hk (query head h reads key head h Hk / Hq).
+ * q_lens, k_lens: device int32 [B], the lengths of a padded batch (NULL: Lq,
+ * Lk).  A row that sees nothing, and a row behind its sequence, gets zeros and
+ * lse = -inf; what the keys and values behind k_lens hold does not matter,
+ * those before it must be finite.  lse: [B, Hq, Lq] fp32, natural logarithm,
+ * nullable.  d 64 or 128, Hq / Hk at most 128.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+AC_API ac_status ac_window_attn_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk, int32_t d,
+                                          const ac_window *w, int64_t *bytes);
+AC_API ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac_view *v, const ac_view *o, float *lse,
+                                int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk, int32_t d,
+                                const int32_t *q_lens, const int32_t *k_lens, const ac_window *w, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+/* Its gradients dq, dk, dv from that of o (d_o), with o and lse as the forward
+ * left them and the same lengths and window.  Key heads shared by several query
+ * heads get the sum.  Rows behind a sequence get zeros.  Bit-identical from run
+ * to run (no atomic sums).  Errors as ac_window_attn. */
+AC_API ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
+                                                   int32_t d, int64_t *bytes);
+AC_API ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *q, const ac_view *k, const ac_view *v,
+                                         const ac_view *o, const float *lse, const ac_view *dq, const ac_view *dk,
+                                         const ac_view *dv, int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
+                                         int32_t d, const int32_t *q_lens, const int32_t *k_lens, const ac_window *w,
+                                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/* A paged cache of keys and values in 8 bits.  k, v: e4m3 codes [pages, heads,
+ * page_tokens, d]; k_scale, v_scale: fp32 [pages, heads], a power of two for
+ * each page and head; a value is code * scale.  page_tokens 16, 32, 64 or 128.
+ * page_table: device int32 [B, max_pages]; token t of sequence b lies in page
+ * page_table[b, t / page_tokens], slot t % page_tokens. */
+typedef struct ac_cache8 {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int32_t pages, heads, page_tokens, d;
+} ac_cache8;
+
+/* Writes the n new tokens of each sequence (k, v: [B, heads, n, d] bf16) behind
+ * its first start[b] (device int32); counts: device int32 [B], how many of the n
+ * are real (NULL: all).  A page's scale is the least power of two 2^e, e in
+ * [-120, 119], that holds its values within 448; when the new tokens of a
+ * part-filled page need a larger one, its earlier codes are converted (exact
+ * but for values that become subnormal).  A NaN stays one, an infinity becomes
+ * the largest value held.  A page that is written belongs to one sequence.
+ * Tokens whose page index is out of range are left out (AC_ERR_BOUNDS).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+AC_API ac_status ac_cache8_append(const ac_cache8 *cache, const ac_view *k, const ac_view *v, int32_t B, int32_t n,
+                                  const int32_t *page_table, int32_t max_pages, const int32_t *start,
+                                  const int32_t *counts, void *stream);
+
+/* ac_window_attn over the cache: q, o [B, Hq, Lq, d] bf16, k_lens (device int32
+ * [B]) the tokens in the cache.  Pages that no query sees are not read, their
+ * table entries may be anything; a visible page whose index is out of range
+ * reads as zeros (AC_ERR_BOUNDS). */
+AC_API ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B, int32_t Hq, int32_t Lq,
+                                          int32_t max_pages, const ac_window *w, int64_t *bytes);
+AC_API ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, const ac_view *o, float *lse, int32_t B,
+                                int32_t Hq, int32_t Lq, const int32_t *page_table, int32_t max_pages,
+                                const int32_t *q_lens, const int32_t *k_lens, const ac_window *w, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+/* Waits for `stream` and reports what kernels of the streaming operators on the
+ * current device have noted since the last call: AC_OK, AC_ERR_TIMEOUT or
+ * AC_ERR_BOUNDS. */
+AC_API ac_status ac_ops_status(void *stream);
 
 #ifdef __cplusplus
 }
