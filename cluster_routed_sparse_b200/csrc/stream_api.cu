@@ -36,6 +36,14 @@ ac_status check_device(const char *fn) {
 
 constexpr int kMaxLen = 1 << 30;
 
+// Few query rows for each key head are bound by reading the keys: they go to
+// the kernel whose products take 16 rows.
+bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= 16; }
+int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
+cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
+    return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);
+}
+
 View view_of(const ac_view *v) { return View{v->data, v->stride_b, v->stride_h, v->stride_l}; }
 
 // 16-byte rows: what the vector and bulk tensor loads need.  A stride of a
@@ -50,8 +58,9 @@ bool rows16(const ac_view *v, int B, int H, int L) {
 }
 
 ac_status window_rule(const ac_window *w, int d, WinRule *out, float *scale) {
-    if (!w || w->left < -1 || w->right < -1 || w->sinks < 0 || w->block < 1 || !std::isfinite(w->scale))
-        return refuse("window: left and right must be >= -1, sinks >= 0, block >= 1 and the scale finite");
+    if (!w || w->left < -1 || w->right < -1 || w->sinks < 0 || w->block < 1 || !std::isfinite(w->scale) ||
+        w->scale < 0.f)
+        return refuse("window: left and right must be >= -1, sinks >= 0, block >= 1 and the scale finite and >= 0");
     *out = WinRule{w->left, w->right, w->sinks, w->block};
     *scale = w->scale != 0.f ? w->scale : 1.f / sqrtf((float)d);
     return AC_OK;
@@ -151,7 +160,9 @@ extern "C" ac_status ac_window_attn_workspace(int32_t B, int32_t Hq, int32_t Hk,
     float scale;
     if (st == AC_OK) st = window_rule(w, d, &r, &scale);
     if (st != AC_OK) return st;
-    *bytes = 0;
+    WinArgs a{};
+    a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d, a.w = r;
+    *bytes = B && Lq ? window_workspace(a) : 0;
     return AC_OK;
 }
 
@@ -177,7 +188,7 @@ extern "C" ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac
     a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
     a.ws = workspace;
     cudaError_t e = op_err_address(&a.err);
-    if (e == cudaSuccess) e = launch_window_simple(a, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_window(a, (cudaStream_t)stream);
     return e == cudaSuccess ? AC_OK : cuda_refuse("ac_window_attn", e);
 }
 
@@ -263,7 +274,10 @@ extern "C" ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B,
     float scale;
     if (st == AC_OK) st = window_rule(w, cache->d, &r, &scale);
     if (st != AC_OK) return st;
-    *bytes = 0;
+    WinArgs a{};
+    a.B = B, a.Hq = Hq, a.Hk = cache->heads, a.G = Hq / cache->heads, a.Lq = Lq, a.d = cache->d, a.w = r;
+    a.Lk = max_pages * cache->page_tokens, a.T = cache->page_tokens, a.k8 = cache->k;
+    *bytes = B && Lq ? window_workspace(a) : 0;
     return AC_OK;
 }
 
@@ -291,6 +305,6 @@ extern "C" ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, co
     a.Lk = max_pages * cache->page_tokens, a.d = cache->d;
     a.ws = workspace;
     cudaError_t e = op_err_address(&a.err);
-    if (e == cudaSuccess) e = launch_window_simple(a, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_window(a, (cudaStream_t)stream);
     return e == cudaSuccess ? AC_OK : cuda_refuse("ac_cache8_attn", e);
 }

@@ -41,6 +41,16 @@ __device__ __forceinline__ int seq_len(const int *lens, int b, int most, OpErr *
     return n < 0 ? 0 : n > most ? most : n;
 }
 
+// 5-D tiled bulk tensor load (coordinates x innermost).  No cluster multicast.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            int32_t v, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+        : "memory");
+}
+
 // ------------------------------------------------------------------ e4m3
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
     uint32_t r;

@@ -27,6 +27,16 @@ struct WinRule {
     int left, right, sinks, g;
 };
 
+// Most tiles of `bn` keys that any `tokens` consecutive queries see.
+inline int64_t window_tiles(const WinRule &w, int64_t tokens, int Lq, int Lk, int bn) {
+    tokens = std::min<int64_t>(std::max(tokens, int64_t(1)), std::max(Lq, 1));
+    if (w.left < 0 || w.right < 0) return (Lk + bn - 1) / bn;
+    const int64_t blocks = (tokens - 1 + w.g - 1) / w.g + 1 + (int64_t)w.left + w.right;
+    const int64_t span = blocks > Lk / w.g ? Lk : std::min<int64_t>(blocks * w.g, Lk);
+    const int64_t sinks = std::min<int64_t>(w.sinks, Lk);
+    return std::min<int64_t>(span / bn + 2 + (sinks + bn - 1) / bn, (Lk + bn - 1) / bn);
+}
+
 struct RopeArgs {
     View x[2], y[2];
     int H[2], B, L, d, P;       // P rotated pairs
@@ -64,7 +74,11 @@ struct WinArgs {
     void *ws;
     OpErr *err;
 };
-cudaError_t launch_window_simple(const WinArgs &a, cudaStream_t s);
+int64_t window_mma_workspace(const WinArgs &a);   // any number of rows
+cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s);
+int64_t window_few_workspace(const WinArgs &a);   // G * Lq <= 16 rows
+cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s);
+cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s);
 
 struct WinBwdArgs {
     WinArgs f;                  // q, k, v, o, lse as the forward left them

@@ -1,6 +1,5 @@
-// window_simple.cu -- attention within a window and over a few first tokens,
-// straight from the definition: one warp per query row (forward, dQ) or key row
-// (dK, dV), fp32 throughout.  The yardstick that the tiled kernels are held to.
+// window_simple.cu -- gradients of the window attention straight from the
+// definition: one warp per query row (dQ) or key row (dK, dV), fp32 throughout.
 #include "stream_device.cuh"
 
 namespace ac {
@@ -13,27 +12,11 @@ __device__ __forceinline__ const bf16 *row_bf16(const View &v, int b, int h, int
     return static_cast<const bf16 *>(v.p) + b * v.b + h * v.h + (int64_t)j * v.l;
 }
 
-// x[0..N) of this lane: elements lane * N .. of a row, from bf16 or from the cache.
+// x[0..N) of this lane: elements lane * N .. of a key or value row.
 template <int N>
 __device__ __forceinline__ void load_row(const WinArgs &a, bool v, int b, int hk, int j, int lane, float (&x)[N]) {
-    if (a.k8) {
-        const int page = a.table[(int64_t)b * a.max_pages + j / a.T];
-        if (page < 0 || page >= a.pages) {
-            atomicOr(&a.err->bits, DEV_ERR_BOUNDS);
-            for (int i = 0; i < N; ++i) x[i] = 0.f;
-            return;
-        }
-        const int64_t slot = (int64_t)page * a.Hk + hk;
-        const uint8_t *c = (v ? a.v8 : a.k8) + (slot * a.T + j % a.T) * a.d + lane * N;
-        const float sc = (v ? a.vs : a.ks)[slot];
-        for (int i = 0; i < N; i += 2) {
-            const float2 f = e4m3x2_to_float2(*reinterpret_cast<const uint16_t *>(c + i));
-            x[i] = f.x * sc, x[i + 1] = f.y * sc;
-        }
-    } else {
-        const bf16 *r = row_bf16(v ? a.v : a.k, b, hk, j) + lane * N;
-        for (int i = 0; i < N; ++i) x[i] = bf2f(r[i]);
-    }
+    const bf16 *r = row_bf16(v ? a.v : a.k, b, hk, j) + lane * N;
+    for (int i = 0; i < N; ++i) x[i] = bf2f(r[i]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -46,35 +29,6 @@ __device__ __forceinline__ float dot(const float (&a)[N], const float (&b)[N]) {
     float s = 0.f;
     for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
     return warp_sum(s);
-}
-
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) k_simple_fwd(const WinArgs a) {
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.Hq * a.Lq) return;
-    const int i = (int)(row % a.Lq), h = (int)(row / a.Lq % a.Hq), b = (int)(row / a.Lq / a.Hq), hk = h / a.G;
-    const int ql = seq_len(a.q_lens, b, a.Lq, a.err), kl = seq_len(a.k_lens, b, a.Lk, a.err);
-    RowRange r{0, 0};
-    if (i < ql) r = row_range(a.w, i + kl - ql, kl);
-    float q[N], o[N], x[N], m = -INFINITY, l = 0.f;
-    const bf16 *qr = row_bf16(a.q, b, h, i) + lane * N;
-    for (int e = 0; e < N; ++e) q[e] = bf2f(qr[e]) * a.scale, o[e] = 0.f;
-    for (int j = min(a.w.sinks, r.lo) > 0 ? 0 : r.lo; j < r.hi; ++j) {
-        if (j >= a.w.sinks && j < r.lo) j = r.lo;
-        if (j >= r.hi) break;
-        load_row(a, false, b, hk, j, lane, x);
-        const float s = dot(q, x);
-        const float mn = fmaxf(m, s), al = __expf(m - mn), p = __expf(s - mn);
-        m = mn;
-        l = l * al + p;
-        load_row(a, true, b, hk, j, lane, x);
-        for (int e = 0; e < N; ++e) o[e] = o[e] * al + p * x[e];
-    }
-    bf16 *dst = static_cast<bf16 *>(a.o.p) + b * a.o.b + h * a.o.h + (int64_t)i * a.o.l + lane * N;
-    for (int e = 0; e < N; ++e) dst[e] = __float2bfloat16_rn(l > 0.f ? o[e] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 template <int D>
@@ -142,16 +96,6 @@ __global__ void __launch_bounds__(32 * kWarps) k_simple_dkv(const WinBwdArgs g) 
 unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-cudaError_t launch_window_simple(const WinArgs &a, cudaStream_t s) {
-    const unsigned n = blocks((int64_t)a.B * a.Hq * a.Lq);
-    if (a.d == 128)
-        k_simple_fwd<128><<<n, 32 * kWarps, 0, s>>>(a);
-    else
-        k_simple_fwd<64><<<n, 32 * kWarps, 0, s>>>(a);
-    AC_NOTE_LAUNCH();
-    return cudaGetLastError();
-}
 
 cudaError_t launch_window_bwd_simple(const WinBwdArgs &g, cudaStream_t s) {
     const WinArgs &a = g.f;

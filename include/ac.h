@@ -456,7 +456,7 @@ AC_API ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view *y,
  * blk(x) = floor(x / block) it sees key j when j < kl, blk(j) <= blk(pos) +
  * right, and blk(j) >= blk(pos) - left or j < sinks.  left, right = -1: no
  * bound on that side; block = tokens per frame makes the window one of whole
- * frames, block = 1 one of tokens.  scale: 0 selects 1/sqrt(d). */
+ * frames, block = 1 one of tokens.  scale >= 0, 0 selects 1/sqrt(d). */
 typedef struct ac_window {
     int32_t left, right, sinks, block;
     float scale;

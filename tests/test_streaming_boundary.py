@@ -54,7 +54,7 @@ BAD_SIZES = [
     (dict(B=1000, Hq=1000, Hk=1000, Lq=1 << 20, Lk=1), INVALID),
     (dict(w=window(left=-2)), INVALID), (dict(w=window(right=-2)), INVALID), (dict(w=window(sinks=-1)), INVALID),
     (dict(w=window(block=0)), INVALID), (dict(w=window(scale=float("inf"))), INVALID), (dict(w=None), INVALID),
-    (dict(q=None), INVALID), (dict(q=view(p=None)), INVALID), (dict(k=view(p=A + 8)), INVALID),
+    (dict(w=window(scale=-0.1)), INVALID), (dict(q=None), INVALID), (dict(q=view(p=None)), INVALID), (dict(k=view(p=A + 8)), INVALID),
     (dict(v=view(l=63)), INVALID), (dict(k=view(h=0)), INVALID), (dict(q=view(l=-64)), INVALID),
     (dict(o=view(h=4)), INVALID),
 ]
