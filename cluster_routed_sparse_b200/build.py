@@ -14,8 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libac.so")
 SOURCES = ["ac_api.cu", "cluster_kernels.cu", "assign_mma.cu", "score_kernels.cu", "quest_mma.cu", "attn_kernel.cu",
-           "noalloc.cu", "stream_api.cu", "rope_axes.cu", "cache8.cu", "window_simple.cu",
-           "window_attn.cu", "window_few.cu"]
+           "noalloc.cu", "stream_api.cu", "rope_axes.cu", "cache8.cu", "window_attn.cu",
+           "window_few.cu", "window_bwd.cu"]
 HEADERS = ["ac_device.cuh", "ac_internal.h", "stream_device.cuh", "stream_internal.h", "stream_host.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -197,7 +197,9 @@ extern "C" ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, in
     if (!bytes) return refuse("ac_window_attn_backward_workspace: NULL argument");
     const ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
     if (st != AC_OK) return st;
-    *bytes = 0;
+    WinArgs a{};
+    a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
+    *bytes = window_bwd_workspace(a);
     return AC_OK;
 }
 
@@ -228,7 +230,7 @@ extern "C" ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *
     a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
     a.ws = workspace;
     cudaError_t e = op_err_address(&a.err);
-    if (e == cudaSuccess) e = launch_window_bwd_simple(g, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_window_bwd(g, (cudaStream_t)stream);
     return e == cudaSuccess ? AC_OK : cuda_refuse("ac_window_attn_backward", e);
 }
 

@@ -84,6 +84,7 @@ struct WinBwdArgs {
     WinArgs f;                  // q, k, v, o, lse as the forward left them
     View go, dq, dk, dv;
 };
-cudaError_t launch_window_bwd_simple(const WinBwdArgs &a, cudaStream_t s);
+int64_t window_bwd_workspace(const WinArgs &a);
+cudaError_t launch_window_bwd(const WinBwdArgs &a, cudaStream_t s);
 
 }  // namespace ac

@@ -16,8 +16,8 @@
 // Warp roles (384 threads, three warpgroups):
 //   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t
 //   warp 9           TMEM allocator and the single-thread tcgen05.mma issuer
-//   bf16 keys:  warp 8 TMA producer; warp 10 zeroes the V rows behind the
-//               sequence (0 x garbage would be NaN), at most once
+//   bf16 keys:  warp 8 TMA producer; in the last tile it zeroes the V rows behind
+//               the sequence (0 x garbage would be NaN)
 //   8-bit keys: warps 8, 10, 11 convert: pages land as codes in a staging
 //               buffer (cp.async.bulk), are multiplied by their scale into bf16
 //               (exact: 4 significant bits, a power of two) and stored in the
@@ -270,12 +270,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
                 int kd = 0, vd = 0;
                 for (int j = 0; j < n_tiles; ++j) {
                     const int s = j % NS, base = tile_base(j);
-                    if (j >= NS && !wait(BAR(B_KE + s), ((j / NS) - 1) & 1)) break;
+                    if (j >= NS && !(ok = wait(BAR(B_KE + s), ((j / NS) - 1) & 1))) break;
                     mbar_arrive_expect_tx(BAR(B_KF + s), LY::TILE);
                     for (int hf = 0; hf < LY::HALVES; ++hf)
                         tma_load_4d(sbase + LY::OFF_K + s * LY::TILE + hf * BN * 128, &maps.k, hf * 64, base, hk, b, BAR(B_KF + s));
                     ++kd;
-                    if (j >= NS && !wait(BAR(B_VE + s), ((j / NS) - 1) & 1)) break;
+                    if (j >= NS && !(ok = wait(BAR(B_VE + s), ((j / NS) - 1) & 1))) break;
                     mbar_arrive_expect_tx(BAR(B_VF + s), LY::TILE);
                     for (int hf = 0; hf < LY::HALVES; ++hf)
                         tma_load_4d(sbase + LY::OFF_V + s * LY::TILE + hf * BN * 128, &maps.v, hf * 64, base, hk, b, BAR(B_VF + s));
@@ -287,10 +287,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
                 wait(BAR(B_QF), 0);
             }
         }
-        if (!C8 && warp == 10 && tail) {
-            const int j = n_tiles - 1, s = j % NS;
-            if (__all_sync(0xFFFFFFFFu, wait(BAR(B_VF + s), (j / NS) & 1))) {
-                const int r0 = kl - tile_base(j);
+        if (!C8 && warp == 8 && tail) {
+            // V rows behind the sequence, by the producer, which has followed every phase
+            __syncwarp();
+            const int j = n_tiles - 1, s = j % NS, r0 = kl - tile_base(j);
+            if (__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+                wait(BAR(B_VF + s), (j / NS) & 1);
                 for (int hf = 0; hf < LY::HALVES; ++hf)
                     for (int i = r0 * 8 + lane; i < BN * 8; i += 32)
                         *reinterpret_cast<uint4 *>(sm + LY::OFF_V + s * LY::TILE + hf * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);

@@ -1,0 +1,635 @@
+// window_bwd.cu -- gradients of the window attention on tcgen05 / TMEM.
+//
+// With P = 2^(s c - lse) from the forward's log-sum-exp, and per row
+// delta = sum_j P dP:
+//   dP = dO V^T    dS = P (dP - delta)    dV = P^T dO    dK = s dS^T Q    dQ = s dS K
+// One kernel in two roles, each with four 128 x 128 products per tile:
+//   rows = queries, tiles = keys:     S = Q K^T, dP = dO V^T, A1 += P K,    A2 += dS K
+//   rows = keys,    tiles = queries:  S = K Q^T, dP = V dO^T, A1 += P dO,   A2 += dS Q
+// (the second holds the transposes of S, P, dP, dS).  Every output row belongs to
+// one CTA: no atomic sums, and the same bits from run to run.  Query rows are
+// packed over the heads of a key head as in window_attn.cu, so the gradients of
+// shared heads add up in the accumulator.
+//
+// The row sum delta0 = sum dO o that the first role starts from uses o as the
+// forward rounded it, off by 2^-9 |dO| |o|: over thousands of keys that error,
+// times sum_j P_j k_j, would be the largest in dQ (1.2e-2 of its norm measured over
+// 5,000 keys, against 2e-3 from all other roundings).  Since sum_j dS_j = 0 for the
+// true delta, r = sum_j dS_j tells the error, and dQ = s (A2 - r A1) takes it
+// out; that is what A1 = P K is for.  r sums dS as rounded to bf16, so that the
+// part of those roundings which is common to all keys leaves too.  The second
+// role takes the corrected delta0 + r.
+//
+// Schedule: A1(j), S(j+1), A2(j), dP(j+1) on the tensor core; 256 threads (row
+// t mod 128, column half t / 128) turn S(j+1) into P while A2(j) and dP(j+1) run,
+// and dP into dS while A1(j+1) and S(j+2) run.  Tensor memory (512 columns):
+// S | dP | A1 | A2, each bf16 operand in the half of its scores that its own
+// threads have read.  P and dS are rounded to bf16 (the operand type), all
+// else is fp32.  Masks as in window_attn.cu: one column interval per thread.
+#include "stream_device.cuh"
+#include "stream_host.h"
+
+namespace ac {
+namespace {
+
+constexpr int NTHREADS = 384;
+constexpr uint32_t kRegsMath = 200, kRegsOther = 72;
+static_assert(2 * 128 * kRegsMath + 128 * kRegsOther <= NTHREADS * 168, "register split exceeds the launch");
+constexpr int kStats = 256;  // floats per query tile: -lse log2(e) of 128 rows, then delta
+
+template <int D>
+struct Layout {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t TILE = HALVES * 128 * 128;
+    static constexpr uint32_t OFF_F = 0;               // fixed tiles F0, F1
+    static constexpr uint32_t OFF_L0 = 2 * TILE;       // [2] looped tiles
+    static constexpr uint32_t OFF_L1 = OFF_L0 + 2 * TILE;
+    static constexpr uint32_t OFF_ST = OFF_L1 + 2 * TILE;  // [2][kStats] statistics of the looped queries
+    static constexpr uint32_t OFF_R = OFF_ST + 2 * kStats * 4;  // [256] row sums
+    static constexpr uint32_t OFF_BAR = OFF_R + 256 * 4;
+    static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
+};
+
+enum {
+    B_FF = 0,   // fixed tiles filled
+    B_0F = 1,   // [2] L0 stage filled
+    B_0E = 3,   // [2] L0 stage free
+    B_1F = 5,   // [2] L1 stage filled
+    B_1E = 7,   // [2] L1 stage free
+    B_SF = 9,   // S written
+    B_DPF = 10, // dP written
+    B_PF = 11,  // P written by the 256 threads
+    B_DF = 12,  // dS written
+    B_Z0 = 13,  // rows behind the sequence zeroed in the last L0, L1 tile
+    B_Z1 = 14,
+    B_AF = 15,  // accumulators complete
+    NBAR = 16
+};
+
+struct BwdMaps {
+    CUtensorMap f0, f1, l0, l1;
+};
+
+struct BwdParams {
+    View dq, dk, dv;
+    float *stats;  // [B Hk][tiles_q][kStats]
+    const int *q_lens, *k_lens;
+    int B, Hq, Hk, G, TT, Lq, Lk, tiles_q, tiles_k;
+    WinRule w;
+    float scale, scale_log2;
+    uint32_t launch;
+    OpErr *err;
+};
+
+__device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Eight tcgen05.mma (TS) into one accumulator; A in two blocks of 32 columns, 64 apart.
+template <uint32_t B_STEP>
+__device__ __forceinline__ void mma8_ts_halves(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 blo, bhi, y, ta;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+        "mov.b64 {blo, bhi}, %2;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 y, blo, %5;\n\tadd.u32 ta, %1, 8;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %6;\n\tadd.u32 ta, %1, 16;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %7;\n\tadd.u32 ta, %1, 24;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %8;\n\tadd.u32 ta, %1, 64;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %9;\n\tadd.u32 ta, %1, 72;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %10;\n\tadd.u32 ta, %1, 80;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
+        "add.u32 y, blo, %11;\n\tadd.u32 ta, %1, 88;\n\tmov.b64 db, {y, bhi};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t}"
+        ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP),
+        "n"(4 * B_STEP), "n"(5 * B_STEP), "n"(6 * B_STEP), "n"(7 * B_STEP)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Tokens of a sequence that see key j: [lo, hi).
+__device__ __forceinline__ RowRange key_range(const WinRule &w, int j, int off, int ql, int kl) {
+    if (j >= kl) return RowRange{0, 0};
+    const long long bj = w.g == 1 ? j : j / w.g;
+    long long lo = w.right < 0 ? 0 : (bj - w.right) * w.g - off;
+    long long hi = w.left < 0 || j < w.sinks ? ql : (bj + w.left + 1) * w.g - off;
+    lo = lo < 0 ? 0 : lo > ql ? ql : lo;
+    hi = hi < lo ? lo : hi > ql ? ql : hi;
+    return RowRange{(int)lo, (int)hi};
+}
+
+// -lse log2(e) (-inf for a row without keys, so that its P is 0) and
+// delta0 = sum dO o of every row of the query tiles, in the order of the tiles.
+// D / 8 lanes per row; bound by reading dO and o once.
+template <int D>
+__global__ void __launch_bounds__(256) k_row_stats(View go, View o, const float *__restrict__ lse, BwdParams p) {
+    constexpr int LPR = D / 8;
+    const int64_t idx = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+    const int part = threadIdx.x % LPR;
+    const int row = (int)(idx % 128);
+    const int64_t tile = idx / 128;
+    const int qt = (int)(tile % p.tiles_q);
+    const int64_t bh = tile / p.tiles_q;
+    if (bh >= (int64_t)p.B * p.Hk) return;  // whole warps: 128 rows of a tile
+    const int b = (int)(bh / p.Hk), hk = (int)(bh % p.Hk);
+    const int i = qt * p.TT + row / p.G, h = hk * p.G + row % p.G;
+    const int ql = seq_len(p.q_lens, b, p.Lq, p.err);
+    const bool live = row < p.G * p.TT && i < ql;
+    float s = 0.f;
+    if (live) {
+        const uint4 x = *(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(go.p) + b * go.b + h * go.h + i * go.l) + part);
+        const uint4 y = *(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(o.p) + b * o.b + h * o.h + i * o.l) + part);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+            s = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), s);
+        }
+    }
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+    if (part == 0) {
+        float nl = -INFINITY;
+        if (live) {
+            const float l = lse[((int64_t)b * p.Hq + h) * p.Lq + i];
+            if (l > -INFINITY) nl = -l * 1.44269504088896f;
+        }
+        float *st = p.stats + tile * kStats;
+        st[row] = nl;
+        st[128 + row] = live ? s : 0.f;
+    }
+}
+
+// KEYS: rows are keys, tiles are queries (dK, dV); otherwise rows are queries (dQ).
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constant__ BwdMaps maps,
+                                                           const __grid_constant__ BwdParams p) {
+    using LY = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- work item: (sequence and key head, row tile).  The row tiles with the most
+    // columns first: early keys (first tokens; no left bound), late queries.
+    const int tiles = KEYS ? p.tiles_k : p.tiles_q;
+    const int bh = blockIdx.x / tiles;
+    const int rt = KEYS ? blockIdx.x % tiles : tiles - 1 - blockIdx.x % tiles;
+    const int b = bh / p.Hk, hk = bh % p.Hk;
+    const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
+    const int off = kl - ql;
+    const int r0 = KEYS ? rt * 128 : rt * p.TT;  // first key, or first token
+
+    int lo_c = 0, n_tiles = 0, nsink = 0;  // lo_c: first tile (behind the first tokens' tiles)
+    bool tail = false;                     // the last tile holds rows behind the sequence that TMA does not zero
+    int tail_row = 0;
+    if (KEYS) {
+        if (r0 < kl) {
+            const RowRange a = key_range(p.w, r0, off, ql, kl);
+            const RowRange z = key_range(p.w, min(r0 + 127, kl - 1), off, ql, kl);
+            const int hi = max(a.hi, z.hi);
+            if (hi > a.lo) lo_c = a.lo / p.TT, n_tiles = (hi + p.TT - 1) / p.TT - lo_c;
+            tail = n_tiles > 0 && (lo_c + n_tiles) * p.TT > ql && ql < p.Lq;
+            tail_row = (ql - (lo_c + n_tiles - 1) * p.TT) * p.G;
+        }
+    } else if (r0 < ql) {
+        const int lo = row_range(p.w, r0 + off, kl).lo;
+        const int hi = row_range(p.w, min(r0 + p.TT, ql) - 1 + off, kl).hi;
+        if (hi > 0) {
+            lo_c = lo / 128;
+            nsink = min((min(p.w.sinks, hi) + 127) / 128, lo_c);
+            n_tiles = nsink + (hi + 127) / 128 - lo_c;
+            tail = (hi + 127) / 128 * 128 > kl && kl < p.Lk;
+            tail_row = kl - (hi + 127) / 128 * 128 + 128;
+        }
+    }
+    // first key of key tile j, or first token of query tile j
+    auto tile_base = [&](int j) { return KEYS ? (lo_c + j) * p.TT : (j < nsink ? j : lo_c + j - nsink) * 128; };
+
+    const uint32_t bar0 = sbase + LY::OFF_BAR;
+#define BAR(i) (bar0 + 8u * (uint32_t)(i))
+    uint32_t *abort_word = &p.err->timeout;
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        const long long c0 = clock64();
+        for (uint32_t it = 0;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 255u) == 255u) {
+                if (*reinterpret_cast<const volatile uint32_t *>(abort_word) == p.launch) return false;
+                if (globaltimer_ns() - t0 > kWaitLimitNs || clock64() - c0 > kWaitLimitCycles || it > kWaitLimitPolls) {
+                    *reinterpret_cast<volatile uint32_t *>(abort_word) = p.launch;
+                    return false;
+                }
+            }
+        }
+    };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
+
+    if (tid == 0) {
+        mbar_init(BAR(B_FF), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(BAR(B_0F + i), 1);
+            mbar_init(BAR(B_0E + i), 1);
+            mbar_init(BAR(B_1F + i), 1);
+            mbar_init(BAR(B_1E + i), 1);
+        }
+        mbar_init(BAR(B_SF), 1);
+        mbar_init(BAR(B_DPF), 1);
+        mbar_init(BAR(B_PF), 256);
+        mbar_init(BAR(B_DF), 256);
+        mbar_init(BAR(B_Z0), 1);
+        mbar_init(BAR(B_Z1), 1);
+        mbar_init(BAR(B_AF), 1);
+        fence_mbar_init();
+    }
+    const int packed = p.G * p.TT;  // rows of a query tile
+    if (KEYS && packed < 128) {
+        // The rows of the query stages that no load fills enter products over
+        // the rows: zeros.
+        for (int t = tid; t < 4 * LY::HALVES * (128 - packed) * 8; t += NTHREADS) {
+            const int i = t % ((128 - packed) * 8), blk = t / ((128 - packed) * 8);
+            *reinterpret_cast<uint4 *>(sm + LY::OFF_L0 + blk * 128 * 128 + packed * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = 0, tP = 128, tA1 = 256, tA2 = 384;
+    bool ok = true;
+
+    if (warp >= 8) {
+        reg_dealloc<kRegsOther>();
+        if (warp == 9 && lane == 0 && n_tiles > 0) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t ISS = idesc_bf16_f32(128, 128, false);
+            constexpr uint32_t ITS = idesc_bf16_f32(128, D, true);
+            const uint64_t f0 = sdesc_sw128(sbase + LY::OFF_F, 16, 1024);
+            const uint64_t f1 = sdesc_sw128(sbase + LY::OFF_F + LY::TILE, 16, 1024);
+            const uint64_t k0 = sdesc_sw128(sbase + LY::OFF_L0, 16, 1024);  // as K-major operands
+            const uint64_t k1 = sdesc_sw128(sbase + LY::OFF_L1, 16, 1024);
+            const uint64_t m0 = sdesc_sw128(sbase + LY::OFF_L0, 128 * 128, 1024);  // as MN-major operands
+            const uint64_t m1 = sdesc_sw128(sbase + LY::OFF_L1, 128 * 128, 1024);
+            constexpr uint64_t STAGE = LY::TILE >> 4;
+            auto scores = [&](uint32_t d, uint64_t f, uint64_t l) {
+                if constexpr (D == 128) {
+                    constexpr uint32_t H = (128 * 128) >> 4;
+                    mma8_ss<2, 4, 6, H, H + 2, H + 4, H + 6, 2, 4, 6, H, H + 2, H + 4, H + 6>(tmem + d, f, l, ISS, 0u);
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_bf16(tmem + d, f + (uint64_t)(kk * 2), l + (uint64_t)(kk * 2), ISS, kk > 0 ? 1u : 0u);
+                }
+            };
+            auto z = [&](int bar, int j) { return !tail || j + 1 < n_tiles || wait(BAR(bar), 0); };
+            ok = wait(BAR(B_FF), 0) && wait(BAR(B_0F), 0) && z(B_Z0, 0);
+            tc_fence_after();
+            if (ok) {
+                scores(tS, f0, k0);
+                tc_commit(BAR(B_SF));
+                ok = wait(BAR(B_1F), 0) && z(B_Z1, 0);
+                tc_fence_after();
+                if (ok) {
+                    scores(tP, f1, k1);
+                    tc_commit(BAR(B_DPF));
+                }
+            }
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                const bool more = j + 1 < n_tiles;
+                const int s = j & 1, s2 = s ^ 1, ph2 = ((j + 1) >> 1) & 1;
+                if (!(ok = wait(BAR(B_PF), j & 1))) break;
+                tc_fence_after();
+                mma8_ts_halves<2048 / 16>(tmem + tA1, tmem + tS, (KEYS ? m1 : m0) + s * STAGE, ITS, j > 0 ? 1u : 0u);
+                tc_commit(BAR(B_1E + s));
+                if (more) {
+                    if (!(ok = wait(BAR(B_0F + s2), ph2) && z(B_Z0, j + 1))) break;
+                    tc_fence_after();
+                    scores(tS, f0, k0 + s2 * STAGE);
+                    tc_commit(BAR(B_SF));
+                }
+                if (!(ok = wait(BAR(B_DF), j & 1))) break;
+                tc_fence_after();
+                mma8_ts_halves<2048 / 16>(tmem + tA2, tmem + tP, m0 + s * STAGE, ITS, j > 0 ? 1u : 0u);
+                tc_commit(BAR(B_0E + s));
+                if (more) {
+                    if (!(ok = wait(BAR(B_1F + s2), ph2) && z(B_Z1, j + 1))) break;
+                    tc_fence_after();
+                    scores(tP, f1, k1 + s2 * STAGE);
+                    tc_commit(BAR(B_DPF));
+                }
+            }
+            tc_commit(BAR(B_AF));
+            wait(BAR(B_AF), 0);
+        } else if (warp == 8 && n_tiles > 0) {
+          if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            const uint32_t qbytes = LY::HALVES * packed * 128;
+            mbar_arrive_expect_tx(BAR(B_FF), 2 * (KEYS ? LY::TILE : qbytes));
+            for (int t = 0; t < 2; ++t)
+                for (int hf = 0; hf < LY::HALVES; ++hf) {
+                    const uint32_t dst = sbase + LY::OFF_F + t * LY::TILE + hf * 128 * 128;
+                    if (KEYS) tma_load_4d(dst, t ? &maps.f1 : &maps.f0, hf * 64, r0, hk, b, BAR(B_FF));
+                    else tma_load_5d(dst, t ? &maps.f1 : &maps.f0, hf * 64, 0, r0, hk, b, BAR(B_FF));
+                }
+            int done[2] = {0, 0};
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                const int s = j & 1, base = tile_base(j);
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= 2 && !(ok = wait(BAR((t ? B_1E : B_0E) + s), ((j >> 1) - 1) & 1))) break;
+                    const uint32_t bar = BAR((t ? B_1F : B_0F) + s);
+                    mbar_arrive_expect_tx(bar, (KEYS ? qbytes : LY::TILE) + (KEYS && t == 0 ? kStats * 4 : 0));
+                    for (int hf = 0; hf < LY::HALVES; ++hf) {
+                        const uint32_t dst = sbase + (t ? LY::OFF_L1 : LY::OFF_L0) + s * LY::TILE + hf * 128 * 128;
+                        if (KEYS) tma_load_5d(dst, t ? &maps.l1 : &maps.l0, hf * 64, 0, base, hk, b, bar);
+                        else tma_load_4d(dst, t ? &maps.l1 : &maps.l0, hf * 64, base, hk, b, bar);
+                    }
+                    if (KEYS && t == 0)
+                        bulk_load(sbase + LY::OFF_ST + s * kStats * 4, p.stats + ((int64_t)bh * p.tiles_q + lo_c + j) * kStats,
+                                  kStats * 4, bar);
+                    ++done[t];
+                }
+            }
+            // Loads still in flight must land before the CTA exits.
+            for (int t = 0; t < 2; ++t)
+                for (int j = max(done[t] - 2, 0); j < done[t]; ++j) wait(BAR((t ? B_1F : B_0F) + (j & 1)), (j >> 1) & 1);
+            wait(BAR(B_FF), 0);
+          }
+          __syncwarp();
+          if (tail && __shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+            // ------------------------------------------------ rows behind the sequence
+            // (by the producer, which has followed every phase of the stages)
+            const int j = n_tiles - 1, s = j & 1;
+            for (int t = 0; t < 2; ++t) {
+                wait(BAR((t ? B_1F : B_0F) + s), (j >> 1) & 1);
+                for (int hf = 0; hf < LY::HALVES; ++hf)
+                    for (int i = max(tail_row, 0) * 8 + lane; i < 128 * 8; i += 32)
+                        *reinterpret_cast<uint4 *>(sm + (t ? LY::OFF_L1 : LY::OFF_L0) + s * LY::TILE + hf * 128 * 128 + i * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(t ? B_Z1 : B_Z0));
+            }
+          }
+        }
+        __syncwarp();
+    } else {
+        reg_alloc<kRegsMath>();
+        // ------------------------------------------------ P and dS; epilogue
+        const int half = warp >> 2, row = tid & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t mS = tmem + lane_off + tS + half * 64, mP = tmem + lane_off + tP + half * 64;
+        float *row_sum = reinterpret_cast<float *>(sm + LY::OFF_R);
+        // KEYS: key r0 + row, its visible tokens; otherwise token and head of the row, its visible keys
+        const int g = row % p.G, i = r0 + row / p.G;
+        RowRange rr{0, 0x7FFFFFFF};  // a row that is not live never makes its warp mask
+        int sink = 0;
+        bool live;
+        float nl = -INFINITY, delta = 0.f, rsum = 0.f;
+        float *stat = p.stats + ((int64_t)bh * p.tiles_q + rt) * kStats;
+        if (KEYS) {
+            live = r0 + row < kl;
+            if (live) rr = key_range(p.w, r0 + row, off, ql, kl);
+        } else {
+            live = row < packed && i < ql;
+            if (live) {
+                rr = row_range(p.w, i + off, kl);
+                sink = min(p.w.sinks, rr.hi);
+                nl = stat[row], delta = stat[128 + row];
+            }
+        }
+        const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+        for (int j = 0; j < n_tiles; ++j) {
+            const int s = j & 1, base = tile_base(j);
+            // columns of this thread that it sees: [c_lo, c_hi) and, of keys, the first ones
+            int c_lo, c_hi, c_sink = 0;
+            bool full;
+            if (KEYS) {
+                const long long lo = (long long)(rr.lo - base) * p.G, hi = (long long)(rr.hi - base) * p.G;
+                full = lo <= 0 && hi >= packed;  // columns behind the packed ones have P = 0
+                c_lo = (int)max(min(lo, 1024ll), -1024ll) - half * 64, c_hi = (int)max(min(hi, 1024ll), -1024ll) - half * 64;
+            } else {
+                full = base + 128 <= rr.hi && (base >= rr.lo || base + 128 <= sink);
+                c_lo = rr.lo - base - half * 64, c_hi = rr.hi - base - half * 64, c_sink = sink - base - half * 64;
+            }
+            if (!live) full = true;
+            const bool masked = !__all_sync(0xFFFFFFFFu, full);
+            const float *st = reinterpret_cast<const float *>(sm + LY::OFF_ST + s * kStats * 4) + half * 64;
+            bool got = wait(BAR(B_SF), j & 1);
+            if (KEYS) got = wait(BAR(B_0F + s), (j >> 1) & 1) && got;  // the statistics came with L0
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t x[2][32];
+            tmem_ld32(mS, x[0]);
+            tmem_ld32(mS + 32, x[1]);
+            tmem_ld_wait();
+            // ---- P = 2^(s c - lse)
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 n4 = make_float4(nl, nl, nl, nl);
+                    if (KEYS) n4 = *reinterpret_cast<const float4 *>(st + c * 32 + e);
+                    float y[4];
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), c2, f2_pack(n4.x, n4.y)), y[0], y[1]);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])), c2, f2_pack(n4.z, n4.w)), y[2], y[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x[c][e + q] = __float_as_uint(ex2_approx(y[q]));
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t vm = (low_mask(c_hi - 32 * c) & ~low_mask(c_lo - 32 * c)) | low_mask(c_sink - 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c][e] = ((vm >> e) & 1u) ? x[c][e] : 0u;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    pk[c * 16 + e / 2] = pack_bf16x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+            tmem_st32(mS, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(BAR(B_PF));
+            // ---- dS = P (dP - delta)
+            if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_DPF), j & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[32];
+                tmem_ld32(mP + c * 32, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 d4 = make_float4(delta, delta, delta, delta);
+                    if (KEYS) d4 = *reinterpret_cast<const float4 *>(st + 128 + c * 32 + e);
+                    float y[4];
+                    f2_unpack(f2_mul(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])),
+                                     f2_sub(f2_pack(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), f2_pack(d4.x, d4.y))), y[0], y[1]);
+                    f2_unpack(f2_mul(f2_pack(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])),
+                                     f2_sub(f2_pack(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3])), f2_pack(d4.z, d4.w))), y[2], y[3]);
+                    const uint32_t w0 = pack_bf16x2(y[0], y[1]), w1 = pack_bf16x2(y[2], y[3]);
+                    pk[c * 16 + e / 2] = w0, pk[c * 16 + e / 2 + 1] = w1;
+                    if (!KEYS)
+                        rsum += (__uint_as_float(w0 << 16) + __uint_as_float(w0 & 0xFFFF0000u)) +
+                                (__uint_as_float(w1 << 16) + __uint_as_float(w1 & 0xFFFF0000u));
+                }
+            }
+            tmem_st32(mP, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(BAR(B_DF));
+        }
+        if (ok && n_tiles > 0 && !__all_sync(0xFFFFFFFFu, wait(BAR(B_AF), 0))) ok = false;
+        tc_fence_after();
+        if (!KEYS) {
+            row_sum[tid] = rsum;
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            rsum = row_sum[row] + row_sum[128 + row];
+            if (half == 0 && live && n_tiles > 0) stat[128 + row] = delta + rsum;
+        }
+        const bool some = live && n_tiles > 0;
+        if (KEYS) {
+            // half 0: dV = A1; half 1: dK = scale A2
+            const View &v = half ? p.dk : p.dv;
+            const float f = half ? p.scale : 1.f;
+            const bool store = ok && r0 + row < p.Lk;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(v.p) + b * v.b + hk * v.h + (int64_t)(r0 + row) * v.l);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (n_tiles > 0) {
+                    tmem_ld32(tmem + lane_off + (half ? tA2 : tA1) + c * 32, o);
+                    tmem_ld_wait();
+                }
+                if (store) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float *x = reinterpret_cast<const float *>(o + 8 * q);
+                        dst[c * 4 + q] = some ? make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                                                           pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f))
+                                              : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+        } else {
+            // dQ = scale (A2 - r A1), half the columns each
+            const bool store = ok && row < packed && i < p.Lq;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.dq.p) + b * p.dq.b + (int64_t)(hk * p.G + g) * p.dq.h +
+                                                   (int64_t)i * p.dq.l + half * (D / 2));
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t a1[32], a2[32];
+                if (n_tiles > 0) {
+                    tmem_ld32(tmem + lane_off + tA1 + half * (D / 2) + c * 32, a1);
+                    tmem_ld32(tmem + lane_off + tA2 + half * (D / 2) + c * 32, a2);
+                    tmem_ld_wait();
+                }
+                if (store) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[e] = p.scale * fmaf(-rsum, __uint_as_float(a1[8 * q + e]), __uint_as_float(a2[8 * q + e]));
+                        dst[c * 4 + q] = some ? make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]))
+                                              : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+#undef BAR
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+int64_t query_tiles(const WinArgs &a) {
+    const int TT = 128 / a.G;
+    return (a.Lq + TT - 1) / TT;
+}
+
+}  // namespace
+
+int64_t window_bwd_workspace(const WinArgs &a) { return (int64_t)a.B * a.Hk * query_tiles(a) * kStats * 4; }
+
+cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
+    const WinArgs &a = g.f;
+    BwdParams p{};
+    p.dq = g.dq, p.dk = g.dk, p.dv = g.dv;
+    p.stats = static_cast<float *>(a.ws);
+    p.q_lens = a.q_lens, p.k_lens = a.k_lens;
+    p.B = a.B, p.Hq = a.Hq, p.Hk = a.Hk, p.G = a.G, p.TT = 128 / a.G, p.Lq = a.Lq, p.Lk = a.Lk;
+    p.tiles_q = (int)query_tiles(a), p.tiles_k = (a.Lk + 127) / 128;
+    p.w = a.w, p.scale = a.scale, p.scale_log2 = a.scale * 1.44269504088896f;
+    p.launch = next_launch_id(), p.err = a.err;
+    const int64_t nq = (int64_t)a.B * a.Hk * p.tiles_q, nk = (int64_t)a.B * a.Hk * p.tiles_k;
+    const int64_t stat_blocks = nq * 128 * (a.d / 8) / 256;
+    if (nq > 0x7FFFFFFF || nk > 0x7FFFFFFF || stat_blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    BwdMaps mq{}, mk{};  // rows = queries; rows = keys
+    cudaError_t e = cudaSuccess;
+    auto qmap = [&](CUtensorMap *m, const View &v) {
+        if (e == cudaSuccess && a.Lq > 0) e = map_rows_packed(m, v, a.B, a.Hk, a.G, a.Lq, a.d, p.TT);
+    };
+    auto kmap = [&](CUtensorMap *m, const View &v) {
+        if (e == cudaSuccess && a.Lk > 0) e = map_rows(m, v, a.B, a.Hk, a.Lk, a.d, 128);
+    };
+    qmap(&mq.f0, a.q), qmap(&mq.f1, g.go), kmap(&mq.l0, a.k), kmap(&mq.l1, a.v);
+    if (e != cudaSuccess) return e;
+    mk.f0 = mq.l0, mk.f1 = mq.l1, mk.l0 = mq.f0, mk.l1 = mq.f1;
+    auto go = [&](auto kern, uint32_t smem, const BwdMaps &m, int64_t grid) {
+        if (e != cudaSuccess || grid == 0) return;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return;
+        kern<<<(unsigned)grid, NTHREADS, smem, s>>>(m, p);
+        AC_NOTE_LAUNCH();
+        e = cudaGetLastError();
+    };
+    if (nq > 0) {
+        if (a.d == 128)
+            k_row_stats<128><<<(unsigned)stat_blocks, 256, 0, s>>>(g.go, a.o, a.lse, p);
+        else
+            k_row_stats<64><<<(unsigned)stat_blocks, 256, 0, s>>>(g.go, a.o, a.lse, p);
+        AC_NOTE_LAUNCH();
+        e = cudaGetLastError();
+    }
+    if (a.d == 128) {
+        go(k_window_bwd<128, false>, Layout<128>::SMEM, mq, nq);
+        go(k_window_bwd<128, true>, Layout<128>::SMEM, mk, nk);
+    } else {
+        go(k_window_bwd<64, false>, Layout<64>::SMEM, mq, nq);
+        go(k_window_bwd<64, true>, Layout<64>::SMEM, mk, nk);
+    }
+    return e;
+}
+
+}  // namespace ac
