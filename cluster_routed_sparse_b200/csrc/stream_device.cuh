@@ -62,10 +62,17 @@ __device__ __forceinline__ uint32_t floats_to_e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     const uint32_t h = e4m3x2_to_half2(two);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
+// Over the cache, values whose page has a scale below 2^-90 count as zeros: the
+// softmax sums divide by the scale and would leave fp32's range.
+constexpr float kMinLogScale = -90.f, kMinScale = 8.077935669463161e-28f;
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 

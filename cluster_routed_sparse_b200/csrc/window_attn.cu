@@ -13,23 +13,34 @@
 // the 128-key tiles that meet any of its rows' and masks columns only in tiles
 // where some row of the warp does not see all of them.
 //
-// Warp roles (384 threads, three warpgroups):
+// Warp roles (three warpgroups; four over 8-bit keys):
 //   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t
+//   warp 8           TMA producer (Q; bf16 keys: K and V, and in the last tile it
+//                    zeroes the V rows behind the sequence: 0 x garbage would be NaN)
 //   warp 9           TMEM allocator and the single-thread tcgen05.mma issuer
-//   bf16 keys:  warp 8 TMA producer; in the last tile it zeroes the V rows behind
-//               the sequence (0 x garbage would be NaN)
-//   8-bit keys: warps 8, 10, 11 convert: pages land as codes in a staging
-//               buffer (cp.async.bulk), are multiplied by their scale into bf16
-//               (exact: 4 significant bits, a power of two) and stored in the
-//               swizzled layout that the products read
+//   8-bit keys: warps 12-15 load the codes of K, warps 8, 10, 11 those of V, into
+//               registers, and store them as fp16 (exact, one conversion for
+//               two codes) in the swizzled layout that the products read.  The
+//               loads of the next tile are in flight while a thread waits for its
+//               stage, and the page numbers and scales of the one after that too.
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P overwrites S as bf16.
 // Few query tiles: the key tiles are split over several CTAs, whose partial O
 // and log-sum-exp k_combine joins.
 //
-// Rounding: P to bf16 (the operand type of the product, 2^-9 relative, random
-// over the keys), O once at the end; everything else is fp32.
+// Over the 8-bit cache the products are fp16 and the scales stay out of them:
+// Q is multiplied by a power of two per row so that it fits (elements below
+// 2^-14 of the row's largest are off by 2^-25 of it), the scale of K goes into the
+// exponent's factor c, and the scale of V, 2^e, into the exponent itself:
+// P = 2^(S c + e - m) with m the running maximum of S c + e, which keeps P in
+// fp16's range whatever the scales are; the sum takes P 2^-e.
+//
+// Rounding: P to bf16 (fp16 over the cache), the operand type of the product,
+// 2^-9 (2^-12) relative and random over the keys; O once at the end; everything
+// else is fp32.
 // Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
 // issued and frees its TMEM.
+#include <type_traits>
+
 #include "stream_device.cuh"
 #include "stream_host.h"
 
@@ -38,11 +49,14 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NS = 2;  // K/V stages
-constexpr int NTHREADS = 384;
-constexpr uint32_t kRegsSoftmax = 200, kRegsOther = 72;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NTHREADS * 168, "register split exceeds the launch");
+template <bool C8>
+struct Split {  // threads and registers: bf16 keys launch with 168 each, 8-bit keys with 128
+    static constexpr int THREADS = C8 ? 512 : 384;
+    static constexpr uint32_t SOFTMAX = C8 ? 152 : 200, OTHER = C8 ? 104 : 72;
+    static_assert(2 * 128 * SOFTMAX + (THREADS - 256) * OTHER <= THREADS * (C8 ? 128 : 168), "register split exceeds the launch");
+};
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kConverters = 96;
+constexpr int kConvK = 128, kConvV = 96;  // converting threads
 
 template <int D, bool C8>
 struct Layout {
@@ -51,9 +65,8 @@ struct Layout {
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = 2 * TILE;
     static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
-    static constexpr uint32_t OFF_ST = OFF_V + NS * TILE;  // 8-bit staging: K codes, V codes
-    static constexpr uint32_t STAGING = C8 ? BN * D : 0;
-    static constexpr uint32_t OFF_BAR = OFF_ST + 2 * STAGING;
+    static constexpr uint32_t OFF_GRP = OFF_V + NS * TILE;  // [4][8] float4: a tile's groups of 16 keys (8-bit keys)
+    static constexpr uint32_t OFF_BAR = OFF_GRP + (C8 ? 4 * 8 * 16 : 0);
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // 1024-byte alignment slack
 };
 static_assert(Layout<128, true>::SMEM <= 232448, "shared memory");
@@ -69,8 +82,8 @@ enum {
     B_OF = 13,    // [2] last PV_i complete (MMA commit)
     B_DONE = 15,  // every MMA complete
     B_VZ = 16,    // V rows behind the sequence zeroed (bf16 keys)
-    B_ST = 17,    // [2] staging of K / V codes filled (8-bit keys)
-    NBAR = 19
+    B_QC = 17,    // query tiles converted to fp16 (8-bit keys)
+    NBAR = 18
 };
 
 struct WinMaps {
@@ -95,16 +108,14 @@ struct WinParams {
 
 __device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+__device__ __forceinline__ uint4 load_codes(const uint8_t *src) {
+    uint4 w;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(src));
+    return w;
 }
 
-__device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
-
 template <int D, bool C8>
-__global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
+__global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
                                                             const __grid_constant__ WinParams p) {
     using LY = Layout<D, C8>;
     extern __shared__ uint8_t smem_raw[];
@@ -159,23 +170,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
         }
     };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
+    float4 *grp_s = reinterpret_cast<float4 *>(sm + LY::OFF_GRP);
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(BAR(B_KF + i), C8 ? kConverters : 1);
+            mbar_init(BAR(B_KF + i), C8 ? kConvK : 1);
             mbar_init(BAR(B_KE + i), 1);
-            mbar_init(BAR(B_VF + i), C8 ? kConverters : 1);
+            mbar_init(BAR(B_VF + i), C8 ? kConvV : 1);
             mbar_init(BAR(B_VE + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(BAR(B_SF + i), 1);
             mbar_init(BAR(B_PF + i), BM);
             mbar_init(BAR(B_OF + i), 1);
-            mbar_init(BAR(B_ST + i), 1);
         }
         mbar_init(BAR(B_QF), 1);
         mbar_init(BAR(B_DONE), 1);
         mbar_init(BAR(B_VZ), 1);
+        mbar_init(BAR(B_QC), has1 ? 2 * BM : BM);
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -189,12 +201,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
     bool ok = true;
 
     if (warp >= 8) {
-        reg_dealloc<kRegsOther>();
+        reg_dealloc<Split<C8>::OTHER>();
         if (warp == 9) {
             // ------------------------------------------------ MMA issuer
             if (lane == 0 && n_tiles > 0) {
-                constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false);
-                constexpr uint32_t IPV = idesc_bf16_f32(BM, D, true);
+                constexpr uint32_t kTypes = C8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 or bf16 operands
+                constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false) & kTypes;
+                constexpr uint32_t IPV = idesc_bf16_f32(BM, D, true) & kTypes;
                 const uint64_t dq0 = sdesc_sw128(sbase + LY::OFF_Q, 16, 1024);
                 const uint64_t dk0 = sdesc_sw128(sbase + LY::OFF_K, 16, 1024);
                 const uint64_t dv0 = sdesc_sw128(sbase + LY::OFF_V, BN * 128, 1024);
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
                     const uint64_t dv = dv0 + (uint64_t)(((j % NS) * LY::TILE) >> 4);
                     mma8_ts<2048 / 16>(tmem + 256 + i * 128, tmem + i * BN, dv, IPV, j > 0 ? 1u : 0u);
                 };
-                ok = wait(BAR(B_QF), 0) && wait(BAR(B_KF), 0);
+                ok = wait(BAR(C8 ? B_QC : B_QF), 0) && wait(BAR(B_KF), 0);
                 tc_fence_after();
                 if (ok) {
                     issue_s(0, 0);
@@ -301,100 +314,98 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
                 if (lane == 0) mbar_arrive(BAR(B_VZ));
             }
         }
-        if (C8 && warp != 9 && n_tiles > 0) {
-            // ------------------------------------------------ 8-bit pages to bf16 tiles
+        if constexpr (C8) {
+            // ------------------------------------------------ 8-bit pages to fp16 tiles
             __syncwarp();
-            const int ct = (warp == 8 ? 0 : warp - 9) * 32 + lane;  // 0..95
-            const int ppt = BN / p.T;                               // pages of a tile
             const int *table = p.table + (int64_t)b * p.max_pages;
-            // Page of the keys from `key` on: -1 where no row of this CTA sees any of
-            // them, -2 when it is visible but its index is out of range.
-            auto page_of = [&](int key) -> int {
-                if (!((key < hi_c && key + p.T > lo_c) || key < sink_c)) return -1;
-                const int page = table[key / p.T];
-                return page < 0 || page >= p.pages ? -2 : page;
-            };
-            auto fetch = [&](int which, int j) {  // thread 0: codes of tile j into the staging
-                const int base = tile_base(j);
-                uint32_t bytes = 0;
-                for (int i = 0; i < ppt; ++i) {
-                    const int page = page_of(base + i * p.T);
-                    if (page >= 0) bytes += p.T * D;
-                    if (page == -2) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
-                }
-                mbar_arrive_expect_tx(BAR(B_ST + which), bytes);
-                for (int i = 0; i < ppt; ++i) {
-                    const int page = page_of(base + i * p.T);
-                    if (page >= 0)
-                        bulk_load(sbase + LY::OFF_ST + which * LY::STAGING + i * p.T * D,
-                                  (which ? p.v8 : p.k8) + ((int64_t)page * p.Hk + hk) * p.T * D, p.T * D, BAR(B_ST + which));
-                }
-            };
-            if (ct == 0) {
-                fetch(0, 0);
-                fetch(1, 0);
-            }
-            int fetched[2] = {1, 1};
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int s = j % NS, base = tile_base(j);
+            const int log_t = 31 - __clz(p.T);
+            // One kind (K or V) of tile after tile; thread ct of NT.
+            auto convert = [&](auto kind, auto nthreads, int ct) {
+                constexpr bool IS_V = decltype(kind)::value;
+                constexpr int NT = decltype(nthreads)::value, CPR = D / 16, NCH = (BN * CPR + NT - 1) / NT;  // 16-code chunks
+                const uint8_t *codes = (IS_V ? p.v8 : p.k8) + (int64_t)hk * p.T * D;
+                const int64_t page_bytes = (int64_t)p.Hk * p.T * D;
+                // Lane i < 8: page of keys 16 i .. 16 i + 15 of tile j, -1 where this CTA sees none of
+                // them (then the table may hold anything) or the index is out of range.
+                auto page_of = [&](int j) -> int {
+                    if (lane >= 8 || j >= n_tiles) return -1;
+                    const int key = (tile_base(j) + 16 * lane) >> log_t << log_t;
+                    if (!((key < hi_c && key + p.T > lo_c) || key < sink_c)) return -1;
+                    const int page = __ldg(table + (key >> log_t));
+                    if (page >= 0 && page < p.pages) return page;
+                    if (!IS_V) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
+                    return -1;
+                };
+                float ks = 1.f, vs = 1.f;  // of this lane's page
+                auto scales_of = [&](int page) {
+                    ks = vs = 1.f;
+                    if (page < 0) return;
+                    if (!IS_V) ks = __ldg(p.ks + (int64_t)page * p.Hk + hk);
+                    vs = __ldg(p.vs + (int64_t)page * p.Hk + hk);
+                };
+                uint4 w[NCH];
+                auto load = [&](int j, int page) {
+                    const int rows = min(kl - tile_base(j), BN);
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    const bool got = wait(BAR(B_ST + which), j & 1) &&
-                                     (j < NS || wait(BAR((which ? B_VE : B_KE) + s), ((j / NS) - 1) & 1));
-                    // the 96 threads leave together
-                    int all = got;
-                    asm volatile("{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\tbarrier.cta.red.and.pred r, 1, 96, q;\n\t"
-                                 "selp.b32 %0, 1, 0, r;\n\t}" : "=r"(all) : "r"((int)got) : "memory");
-                    if (!all) {
+                    for (int k = 0; k < NCH; ++k) {
+                        const int c = ct + NT * k, r = c / CPR;
+                        const int pg = __shfl_sync(0xFFFFFFFFu, page, (r >> 4) & 7);
+                        w[k] = make_uint4(0, 0, 0, 0);
+                        if (pg >= 0 && r < rows) w[k] = load_codes(codes + pg * page_bytes + (r & (p.T - 1)) * D + (c % CPR) * 16);
+                    }
+                };
+                int page = page_of(0), next = page_of(1);
+                scales_of(page);
+                if (IS_V && vs < kMinScale) page = -1;
+                load(0, page);
+                for (int j = 0; j < n_tiles; ++j) {
+                    const int s = j % NS;
+                    if (!__all_sync(0xFFFFFFFFu, j < NS || wait(BAR((IS_V ? B_VE : B_KE) + s), ((j / NS) - 1) & 1))) {
                         ok = false;
                         break;
                     }
-                    uint8_t *dst = sm + (which ? LY::OFF_V : LY::OFF_K) + s * LY::TILE;
-                    const uint8_t *src = sm + LY::OFF_ST + which * LY::STAGING;
-                    constexpr int CPR = D / 16;  // 16-code chunks of a row
-                    for (int c = ct; c < BN * CPR; c += kConverters) {
-                        const int r = c / CPR, e = c % CPR;
-                        const int page = base + r < kl ? page_of((base + r) / p.T * p.T) : -1;
-                        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-                        if (page >= 0) {
-                            const float sc = (which ? p.vs : p.ks)[(int64_t)page * p.Hk + hk];
-                            const uint4 w = *reinterpret_cast<const uint4 *>(src + c * 16);
-                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                            uint32_t q[8];
-                            const uint64_t sc2 = f2_pack(sc, sc);
+                    if (!IS_V && ct < 8) {
+                        // What the softmax needs of the group: the scale of K, the exponent of the
+                        // scale of V and its inverse.  (The slot's last readers are four tiles back.)
+                        const float ev = fmaxf(__log2f(vs), kMinLogScale);
+                        grp_s[(j & 3) * 8 + ct] = make_float4(ks, ev, ex2_approx(-ev), 0.f);
+                    }
+                    uint8_t *dst = sm + (IS_V ? LY::OFF_V : LY::OFF_K) + s * LY::TILE;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 f = e4m3x2_to_float2((u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                                float x, y;
-                                f2_unpack(f2_mul(f2_pack(f.x, f.y), sc2), x, y);
-                                q[i] = pack_bf16x2(x, y);
-                            }
-                            w0 = make_uint4(q[0], q[1], q[2], q[3]), w1 = make_uint4(q[4], q[5], q[6], q[7]);
-                        }
+                    for (int k = 0; k < NCH; ++k) {
+                        const int c = ct + NT * k, r = c / CPR, e = c % CPR;
+                        if (c >= BN * CPR) break;
                         // 128-byte rows of a column half, 16-byte pieces swizzled by the row
                         uint8_t *row = dst + (e / 4) * BN * 128 + r * 128;
                         const int a = (e % 4) * 2;
-                        *reinterpret_cast<uint4 *>(row + ((a ^ (r & 7)) << 4)) = w0;
-                        *reinterpret_cast<uint4 *>(row + (((a + 1) ^ (r & 7)) << 4)) = w1;
+                        *reinterpret_cast<uint4 *>(row + ((a ^ (r & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_half2(w[k].x & 0xFFFFu), e4m3x2_to_half2(w[k].x >> 16),
+                                       e4m3x2_to_half2(w[k].y & 0xFFFFu), e4m3x2_to_half2(w[k].y >> 16));
+                        *reinterpret_cast<uint4 *>(row + (((a + 1) ^ (r & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_half2(w[k].z & 0xFFFFu), e4m3x2_to_half2(w[k].z >> 16),
+                                       e4m3x2_to_half2(w[k].w & 0xFFFFu), e4m3x2_to_half2(w[k].w >> 16));
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(BAR((which ? B_VF : B_KF) + s));
-                    converters_sync();  // the staging has been read
-                    if (ct == 0 && j + 1 < n_tiles) {
-                        fetch(which, j + 1);
-                        ++fetched[which];
+                    mbar_arrive(BAR((IS_V ? B_VF : B_KF) + s));
+                    if (j + 1 < n_tiles) {
+                        page = next;
+                        next = page_of(j + 2);
+                        scales_of(page);
+                        // (the V page's scale decides whether its codes count: it is waited for here)
+                        if (IS_V && vs < kMinScale) page = -1;
+                        load(j + 1, page);
                     }
                 }
-            }
-            if (ct == 0) {
-                // Loads still in flight must land before the CTA exits.
-                for (int which = 0; which < 2; ++which) wait(BAR(B_ST + which), (fetched[which] - 1) & 1);
-                wait(BAR(B_QF), 0);
+            };
+            if (n_tiles > 0) {
+                if (warp >= 12) convert(std::false_type{}, std::integral_constant<int, kConvK>{}, tid - 384);
+                else if (warp != 9) convert(std::true_type{}, std::integral_constant<int, kConvV>{}, (warp == 8 ? 0 : warp - 9) * 32 + lane);
+                if (warp == 8 && lane == 0) wait(BAR(B_QF), 0);  // in flight until then
             }
         }
         __syncwarp();
     } else {
-        reg_alloc<kRegsSoftmax>();
+        reg_alloc<Split<C8>::SOFTMAX>();
         // ------------------------------------------------ softmax + epilogue
         const int wg = warp >> 2;
         const int row = tid & 127;
@@ -412,41 +423,91 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
         const uint32_t tO = tmem + lane_off + 256 + wg * 128;
         const bool active = n_tiles > 0 && (wg == 0 || has1);
         if (active) {
-            const float sl2 = p.scale_log2;
-            for (int j = 0; j < n_tiles; ++j) {
+            float sl2 = p.scale_log2;
+            if (C8) {
+                // This thread's row of Q to fp16, scaled by a power of two to below 2.
+                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_QF), 0))) ok = false;
+                uint8_t *qrow = sm + LY::OFF_Q + wg * LY::TILE + row * 128;
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(qrow + (c / 8) * BM * 128 + (((c % 8) ^ (row & 7)) << 4));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+                }
+                const int ex = min(max((int)(top >> 7) - 127, -120), 120);
+                const float dn = exp2i(-ex);
+                sl2 *= exp2i(ex);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 *at = reinterpret_cast<uint4 *>(qrow + (c / 8) * BM * 128 + (((c % 8) ^ (row & 7)) << 4));
+                    const uint4 w = *at;
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = pack_half2(__uint_as_float(u[e] << 16) * dn, __uint_as_float(u[e] & 0xFFFF0000u) * dn);
+                    *at = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(BAR(B_QC));
+            }
+            for (int j = 0; j < n_tiles && ok; ++j) {
                 // Wait outcomes are combined across the warp: the TMEM loads and
                 // stores below are warp-collective, so a warp leaves together.
-                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_SF + wg), j & 1))) {
+                bool got = wait(BAR(B_SF + wg), j & 1);
+                if (C8) got = wait(BAR(B_KF + j % NS), (j / NS) & 1) && got;  // the tile's groups came with K
+                if (!__all_sync(0xFFFFFFFFu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t r[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, r[c]);
                 const int base = tile_base(j);
                 const bool full = base + BN <= rr.hi && (base >= rr.lo || base + BN <= sink);
                 const bool masked = !__all_sync(0xFFFFFFFFu, full);
-                tmem_ld_wait();
-                if (masked) {
+                // The scores are read 64 columns at a time.  Over bf16 keys all 128 stay
+                // in registers; over the cache, whose converting threads need registers
+                // too, they are read again for the exponentials.
+                constexpr int KEEP = C8 ? 2 : 4;
+                uint32_t r[KEEP][32];
+                auto read = [&](int c0, int n) {
+                    for (int c = 0; c < n; ++c) tmem_ld32(tS + (c0 + c) * 32, r[(c0 + c) % KEEP]);
+                    tmem_ld_wait();
+                    if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int cb = base + 32 * c;
-                        const uint32_t vm = (low_mask(rr.hi - cb) & ~low_mask(rr.lo - cb)) | low_mask(sink - cb);
+                        for (int c = 0; c < n; ++c) {
+                            const int cb = base + 32 * (c0 + c);
+                            const uint32_t vm = (low_mask(rr.hi - cb) & ~low_mask(rr.lo - cb)) | low_mask(sink - cb);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) r[c][e] = ((vm >> e) & 1u) ? r[c][e] : 0xFF800000u;
+                            for (int e = 0; e < 32; ++e) {
+                                uint32_t &x = r[(c0 + c) % KEEP][e];
+                                x = ((vm >> e) & 1u) ? x : 0xFF800000u;
+                            }
+                        }
                     }
-                }
+                };
+                // row maximum: eight independent ones, over the cache those of the groups of 16 keys
                 float pm[8];
 #pragma unroll
                 for (int a = 0; a < 8; ++a) pm[a] = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c0 = 0; c0 < 4; c0 += KEEP) {
+                    read(c0, KEEP);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        pm[(e >> 1) & 7] = fmax3(pm[(e >> 1) & 7], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
+                    for (int c = c0; c < c0 + KEEP; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const int a = C8 ? 2 * c + (e >> 4) : (e >> 1) & 7;
+                            pm[a] = fmax3(pm[a], __uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1]));
+                        }
+                }
+                const float4 *grp = grp_s + (j & 3) * 8;
+                if (C8) {
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) pm[a] = fmaf(pm[a], sl2 * grp[a].x, grp[a].y);
+                }
                 const float tmax = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-                const float m_new = fmaxf(m_run, tmax * sl2);
+                const float m_new = fmaxf(m_run, C8 ? tmax : tmax * sl2);
                 // The rescale touches TMEM with warp-collective loads and stores, so
                 // the whole warp moves when one live row's maximum grew by more than 2^8.
                 if (__any_sync(0xFFFFFFFFu, j == 0 || (live && m_new > m_run + kRescaleLog2))) {
@@ -467,24 +528,38 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
                     m_run = m_new;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;  // nothing seen yet: every p is 0
-                const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
+                uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
                 uint64_t ps2[4];
+                float l_tile = 0.f;  // over the cache: the groups' sums, without their scales
 #pragma unroll
                 for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    if (C8) read(half * 2, 2);
                     uint32_t pk[32];
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         const int c = half * 2 + cc;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])), sl2x2, negm2);
+                            if (C8 && e % 16 == 0) {
+                                const float4 f = grp[2 * c + e / 16];
+                                const float k = sl2 * f.x, n = f.y - m_use;
+                                sl2x2 = f2_pack(k, k), negm2 = f2_pack(n, n);
+                            }
+                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1])), sl2x2, negm2);
                             float x0, x1;
                             f2_unpack(x2, x0, x1);
                             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                             ps2[(e >> 1) & 3] = f2_add(ps2[(e >> 1) & 3], f2_pack(p0, p1));
-                            pk[cc * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
+                            pk[cc * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
+                            if (C8 && e % 16 == 14) {
+                                float a0, a1;
+                                f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
+                                l_tile = fmaf(a0 + a1, grp[2 * c + e / 16].z, l_tile);
+#pragma unroll
+                                for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
+                            }
                         }
                     }
                     tmem_st32(tS + half * 32, pk);
@@ -493,7 +568,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_attn(const __grid_consta
 #pragma unroll
                 for (int a = 0; a < 4; ++a) f2_unpack(ps2[a], ps[2 * a], ps[2 * a + 1]);
                 tmem_st_wait();
-                l_run += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+                l_run += C8 ? l_tile : ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
                 tc_fence_before();
                 mbar_arrive(BAR(B_PF + wg));
             }
@@ -657,7 +732,7 @@ cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s) {
     auto go = [&](auto kern, uint32_t smem) -> cudaError_t {
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
-        kern<<<(unsigned)grid, NTHREADS, smem, s>>>(maps, p);
+        kern<<<(unsigned)grid, a.k8 ? Split<true>::THREADS : Split<false>::THREADS, smem, s>>>(maps, p);
         AC_NOTE_LAUNCH();
         return cudaGetLastError();
     };

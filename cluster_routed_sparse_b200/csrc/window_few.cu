@@ -16,10 +16,8 @@
 // The keys are split over CTAs (k_combine joins them) and, within a CTA, over
 // four warps, which are joined in shared memory.
 //
-// Rounding: over the 8-bit cache Q enters as fp16 scaled by a power of two per
-// row (exact for elements within 2^-14 of the row's largest, off by 2^-25 of it
-// otherwise), codes are exact in fp16 and bf16, scales go to the fp32 scores and
-// weights; P to bf16, as in the tile kernel.
+// Types, scales and roundings as in the tile kernel: bf16 over bf16 keys, fp16 with
+// the scales in the exponents over the 8-bit cache.
 #include "stream_device.cuh"
 
 namespace ac {
@@ -124,8 +122,7 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
             const float dn = exp2i(-ex);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-                const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
-                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
             }
         }
 #pragma unroll
@@ -149,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
             const int64_t slot = (int64_t)page * p.Hk + hk;
             ksc = __ldg(p.ks + slot), vsc = __ldg(p.vs + slot);
             const int64_t at = (slot * p.T + base % p.T) * D;
-            return Rows{p.k8 + at, p.v8 + at};
+            return Rows{p.k8 + at, vsc >= kMinScale ? p.v8 + at : nullptr};
         } else {
             const bf16 *k = static_cast<const bf16 *>(p.k.p) + b * p.k.b + hk * p.k.h + (int64_t)base * p.k.l;
             const bf16 *v = static_cast<const bf16 *>(p.v.p) + b * p.v.b + hk * p.v.h + (int64_t)base * p.v.l;
@@ -235,9 +232,10 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
                         s[u][2 * e + x] = see ? s[u][2 * e + x] : -INFINITY;
                     }
         }
+        const float ev = C8 ? fmaxf(__log2f(vs), kMinLogScale) : 0.f;  // exponent of the scale of V
         float top[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) top[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        for (int e = 0; e < 2; ++e) top[e] = ev + fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
         // The maximum moves when some row's grew by more than 2^8 (or is the first).
         if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
@@ -254,15 +252,18 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
             }
         }
         uint32_t ap[4];
+        const float inv_vs = C8 ? ex2_approx(-ev) : 1.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float mu = m[e] == -INFINITY ? 0.f : m[e];
+            const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
+            float sum = 0.f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float p0 = ex2_approx(s[u][2 * e] - mu), p1 = ex2_approx(s[u][2 * e + 1] - mu);
-                l[e] += p0 + p1;
-                ap[2 * u + e] = C8 ? pack_bf16x2(p0 * vs, p1 * vs) : pack_bf16x2(p0, p1);
+                sum += p0 + p1;
+                ap[2 * u + e] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
             }
+            l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
         }
         // n8 tile n, column g8 is output element g8 D/8 + n
 #pragma unroll
@@ -273,17 +274,20 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
                 const uint32_t sel = odd ? 0x7362 : 0x5140;
                 const uint32_t x = __byte_perm(vw[0][word], vw[1][word], sel), y = __byte_perm(vw[2][word], vw[3][word], sel);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 fx = e4m3x2_to_float2((x >> (16 * i)) & 0xFFFFu), fy = e4m3x2_to_float2((y >> (16 * i)) & 0xFFFFu);
-                    b0[i] = pack_bf16x2(fx.x, fx.y), b1[i] = pack_bf16x2(fy.x, fy.y);
-                }
+                for (int i = 0; i < 2; ++i)
+                    b0[i] = e4m3x2_to_half2((x >> (16 * i)) & 0xFFFFu), b1[i] = e4m3x2_to_half2((y >> (16 * i)) & 0xFFFFu);
             } else {
                 const uint32_t r0 = vw[0][n / 2], r1 = vw[1][n / 2], r2 = vw[2][n / 2], r3 = vw[3][n / 2];
                 b0[0] = __byte_perm(r0, r1, 0x5410), b0[1] = __byte_perm(r0, r1, 0x7632);
                 b1[0] = __byte_perm(r2, r3, 0x5410), b1[1] = __byte_perm(r2, r3, 0x7632);
             }
-            mma_bf16(acc[n], ap, b0[0], b1[0]);
-            mma_bf16(acc[n + 1], ap, b0[1], b1[1]);
+            if constexpr (C8) {
+                mma_f16(acc[n], ap, b0[0], b1[0]);
+                mma_f16(acc[n + 1], ap, b0[1], b1[1]);
+            } else {
+                mma_bf16(acc[n], ap, b0[0], b1[0]);
+                mma_bf16(acc[n + 1], ap, b0[1], b1[1]);
+            }
         }
         if (more) load_v(nxt, base2);
         ks = ks_next, vs = vs_next;

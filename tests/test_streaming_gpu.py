@@ -408,6 +408,31 @@ def test_cache8_attn(case, T):
     ref.check("lse", lse, r)
 
 
+@pytest.mark.parametrize("Lq", [1, 40])
+def test_cache8_attn_scales_of_very_different_size(Lq):
+    """Pages of zeros (the smallest scale), pages 2^40 apart, and queries of any size."""
+    B, H, T, d, n = 1, 2, 16, 64, 200
+    g = gen(61)
+    c = random_cache(g, 13, H, T, d)
+    e = torch.randint(-20, 20, (13, H), generator=g, device="cuda").float()
+    c.v_scale.copy_(torch.exp2(e))
+    c.k_scale.copy_(torch.exp2(torch.randint(-12, -6, (13, H), generator=g, device="cuda").float()))
+    c.v[3] = 0
+    c.v_scale[3] = 2.0 ** -120
+    c.v.view(torch.uint8)[:, 1] = 0  # a whole head of zeros
+    c.v_scale[:, 1] = 2.0 ** -120
+    table = torch.arange(13, device="cuda", dtype=torch.int32).view(1, 13)
+    lens = torch.tensor([n], device="cuda", dtype=torch.int32)
+    for size in (2.0 ** -20, 1.0, 2.0 ** 4):
+        q = normal(g, B, H, Lq, d) * size
+        o, lse = crs.cache8_attn(q, c, table, lens, return_lse=True)
+        k, v = dense(c, table, n)
+        r = ref.attention(q, k, v, ref.visible(B, Lq, n, -1, 0, 0, 1))
+        ref.check("lse", lse, r)
+        ref.check("o", o, r)
+        assert not o[:, 1].any()
+
+
 # ------------------------------------------------------------------ together
 def test_streaming_generation_and_training_step():
     """Frame after frame: rotate, attend within the window over the cache, append; the rotation and the window
