@@ -51,6 +51,68 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int3
         : "memory");
 }
 
+// ------------------------------------------------------------------ products
+// The issuing warp stays converged and its descriptors are the same in every
+// lane, so that they live in uniform registers; one elected lane executes the
+// instruction.  (A branch to a single lane costs moves to uniform registers for
+// every operand of every product: 3,500 cycles of issue per pair of 128-key tiles
+// instead of the 2,048 that the products take.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+struct Desc {  // shared-memory matrix descriptor; offsets in 16-byte units stay within the low word
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc make_desc(uint64_t d) { return Desc{(uint32_t)d, (uint32_t)(d >> 32)}; }
+
+// D[tmem] (+)= A[smem] B[smem]^T, one K16 step
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]^T, one K16 step
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+        : "memory");
+}
+// Two K-major operands of 128 rows, D / 64 column halves 16 KB apart, 128-byte swizzle.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, Desc a, Desc b, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = (k / 4) * ((128 * 128) >> 4) + (k % 4) * 2;
+        mma_ss(leader, d, Desc{a.lo + at, a.hi}, Desc{b.lo + at, b.hi}, idesc, k > 0 ? 1u : 0u);
+    }
+}
+// A: 128 x 128 16-bit values in tensor memory, 32 columns for each 64 of K, A_STEP columns apart;
+// B: 128 rows (K) in shared memory, MN-major.
+template <int A_STEP>
+__device__ __forceinline__ void mma_weights(uint32_t leader, uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        mma_ts(leader, d, a + (k / 4) * A_STEP + (k % 4) * 8, Desc{b.lo + k * (2048 >> 4), b.hi}, idesc, k > 0 ? 1u : accumulate);
+}
+
 // ------------------------------------------------------------------ e4m3
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
     uint32_t r;

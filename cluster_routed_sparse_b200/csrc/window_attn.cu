@@ -17,7 +17,7 @@
 //   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t
 //   warp 8           TMA producer (Q; bf16 keys: K and V, and in the last tile it
 //                    zeroes the V rows behind the sequence: 0 x garbage would be NaN)
-//   warp 9           TMEM allocator and the single-thread tcgen05.mma issuer
+//   warp 9           TMEM allocator and tcgen05.mma issuer
 //   8-bit keys: warps 12-15 load the codes of K, warps 8, 10, 11 those of V, into
 //               registers, and store them as fp16 (exact, one conversion for
 //               two codes) in the swizzled layout that the products read.  The
@@ -204,69 +204,57 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
         reg_dealloc<Split<C8>::OTHER>();
         if (warp == 9) {
             // ------------------------------------------------ MMA issuer
-            if (lane == 0 && n_tiles > 0) {
+            // (the whole warp, with the same values in every lane: see stream_device.cuh)
+            const int n = uniform(n_tiles), two = uniform(has1), clean = uniform(tail);
+            if (n > 0) {
                 constexpr uint32_t kTypes = C8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 or bf16 operands
                 constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false) & kTypes;
                 constexpr uint32_t IPV = idesc_bf16_f32(BM, D, true) & kTypes;
-                const uint64_t dq0 = sdesc_sw128(sbase + LY::OFF_Q, 16, 1024);
-                const uint64_t dk0 = sdesc_sw128(sbase + LY::OFF_K, 16, 1024);
-                const uint64_t dv0 = sdesc_sw128(sbase + LY::OFF_V, BN * 128, 1024);
+                constexpr uint32_t STEP = LY::TILE >> 4;
+                const uint32_t leader = elect_one();
+                const Desc dq0 = make_desc(sdesc_sw128(sbase + LY::OFF_Q, 16, 1024));
+                const Desc dk0 = make_desc(sdesc_sw128(sbase + LY::OFF_K, 16, 1024));
+                const Desc dv0 = make_desc(sdesc_sw128(sbase + LY::OFF_V, BN * 128, 1024));
+                auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(BAR(bar), parity)) != 0; };
+                // (all 512 columns are this CTA's: tensor memory starts at address 0)
                 auto issue_s = [&](int i, int j) {
-                    const uint64_t dq = dq0 + (uint64_t)((i * LY::TILE) >> 4);
-                    const uint64_t dk = dk0 + (uint64_t)(((j % NS) * LY::TILE) >> 4);
-                    if constexpr (D == 128) {
-                        constexpr uint32_t H = (BM * 128) >> 4;  // second column half
-                        mma8_ss<2, 4, 6, H, H + 2, H + 4, H + 6, 2, 4, 6, H, H + 2, H + 4, H + 6>(tmem + i * BN, dq, dk, IQK, 0u);
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_bf16(tmem + i * BN, dq + (uint64_t)(kk * 2), dk + (uint64_t)(kk * 2), IQK, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(BAR(B_SF + i));
+                    mma_rows<D>(leader, i * BN, Desc{dq0.lo + i * STEP, dq0.hi}, Desc{dk0.lo + (j % NS) * STEP, dk0.hi}, IQK);
+                    commit(leader, BAR(B_SF + i));
                 };
                 auto issue_pv = [&](int i, int j) {
-                    const uint64_t dv = dv0 + (uint64_t)(((j % NS) * LY::TILE) >> 4);
-                    mma8_ts<2048 / 16>(tmem + 256 + i * 128, tmem + i * BN, dv, IPV, j > 0 ? 1u : 0u);
+                    mma_weights<32>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV, j > 0 ? 1u : 0u);
                 };
-                ok = wait(BAR(C8 ? B_QC : B_QF), 0) && wait(BAR(B_KF), 0);
+                bool go = wait_all(C8 ? B_QC : B_QF, 0) && wait_all(B_KF, 0);
                 tc_fence_after();
-                if (ok) {
+                if (go) {
                     issue_s(0, 0);
-                    if (has1) issue_s(1, 0);
-                    tc_commit(BAR(B_KE));
+                    if (two) issue_s(1, 0);
+                    commit(leader, BAR(B_KE));
                 }
-                for (int j = 0; j < n_tiles && ok; ++j) {
-                    const bool more = j + 1 < n_tiles;
-                    if (!wait(BAR(B_PF), j & 1) || !wait(BAR(B_VF + j % NS), (j / NS) & 1) ||
-                        (tail && !more && !wait(BAR(B_VZ), 0))) {
-                        ok = false;
+                for (int j = 0; j < n && go; ++j) {
+                    const bool more = j + 1 < n;
+                    if (!(go = wait_all(B_PF, j & 1) && wait_all(B_VF + j % NS, (j / NS) & 1) &&
+                               (!clean || more || wait_all(B_VZ, 0))))
                         break;
-                    }
                     tc_fence_after();
                     issue_pv(0, j);
-                    if (!more) tc_commit(BAR(B_OF));
+                    if (!more) commit(leader, BAR(B_OF));
                     if (more) {
-                        if (!wait(BAR(B_KF + (j + 1) % NS), ((j + 1) / NS) & 1)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!(go = wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))) break;
                         tc_fence_after();
                         issue_s(0, j + 1);
                     }
-                    if (has1) {
-                        if (!wait(BAR(B_PF + 1), j & 1)) {
-                            ok = false;
-                            break;
-                        }
+                    if (two) {
+                        if (!(go = wait_all(B_PF + 1, j & 1))) break;
                         tc_fence_after();
                         issue_pv(1, j);
-                        if (!more) tc_commit(BAR(B_OF + 1));
+                        if (!more) commit(leader, BAR(B_OF + 1));
                         if (more) issue_s(1, j + 1);
                     }
-                    if (more) tc_commit(BAR(B_KE + (j + 1) % NS));
-                    tc_commit(BAR(B_VE + j % NS));
+                    if (more) commit(leader, BAR(B_KE + (j + 1) % NS));
+                    commit(leader, BAR(B_VE + j % NS));
                 }
-                tc_commit(BAR(B_DONE));
+                commit(leader, BAR(B_DONE));
                 wait(BAR(B_DONE), 0);
             }
             __syncwarp();

@@ -83,33 +83,6 @@ struct BwdParams {
 
 __device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
-// Eight tcgen05.mma (TS) into one accumulator; A in two blocks of 32 columns, 64 apart.
-template <uint32_t B_STEP>
-__device__ __forceinline__ void mma8_ts_halves(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, t;\n\t.reg .b32 blo, bhi, y, ta;\n\t.reg .b64 db;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-        "mov.b64 {blo, bhi}, %2;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "add.u32 y, blo, %5;\n\tadd.u32 ta, %1, 8;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %6;\n\tadd.u32 ta, %1, 16;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %7;\n\tadd.u32 ta, %1, 24;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %8;\n\tadd.u32 ta, %1, 64;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %9;\n\tadd.u32 ta, %1, 72;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %10;\n\tadd.u32 ta, %1, 80;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t"
-        "add.u32 y, blo, %11;\n\tadd.u32 ta, %1, 88;\n\tmov.b64 db, {y, bhi};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, t;\n\t}"
-        ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP),
-        "n"(4 * B_STEP), "n"(5 * B_STEP), "n"(6 * B_STEP), "n"(7 * B_STEP)
-        : "memory");
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -270,71 +243,68 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tS = 0, tP = 128, tA1 = 256, tA2 = 384;
+    constexpr uint32_t tS = 0, tP = 128, tA1 = 256, tA2 = 384;  // (all 512 columns are this CTA's: they start at 0)
     bool ok = true;
 
     if (warp >= 8) {
         reg_dealloc<kRegsOther>();
-        if (warp == 9 && lane == 0 && n_tiles > 0) {
+        if (warp == 9) {
             // ------------------------------------------------ MMA issuer
-            constexpr uint32_t ISS = idesc_bf16_f32(128, 128, false);
-            constexpr uint32_t ITS = idesc_bf16_f32(128, D, true);
-            const uint64_t f0 = sdesc_sw128(sbase + LY::OFF_F, 16, 1024);
-            const uint64_t f1 = sdesc_sw128(sbase + LY::OFF_F + LY::TILE, 16, 1024);
-            const uint64_t k0 = sdesc_sw128(sbase + LY::OFF_L0, 16, 1024);  // as K-major operands
-            const uint64_t k1 = sdesc_sw128(sbase + LY::OFF_L1, 16, 1024);
-            const uint64_t m0 = sdesc_sw128(sbase + LY::OFF_L0, 128 * 128, 1024);  // as MN-major operands
-            const uint64_t m1 = sdesc_sw128(sbase + LY::OFF_L1, 128 * 128, 1024);
-            constexpr uint64_t STAGE = LY::TILE >> 4;
-            auto scores = [&](uint32_t d, uint64_t f, uint64_t l) {
-                if constexpr (D == 128) {
-                    constexpr uint32_t H = (128 * 128) >> 4;
-                    mma8_ss<2, 4, 6, H, H + 2, H + 4, H + 6, 2, 4, 6, H, H + 2, H + 4, H + 6>(tmem + d, f, l, ISS, 0u);
-                } else {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_bf16(tmem + d, f + (uint64_t)(kk * 2), l + (uint64_t)(kk * 2), ISS, kk > 0 ? 1u : 0u);
-                }
-            };
-            auto z = [&](int bar, int j) { return !tail || j + 1 < n_tiles || wait(BAR(bar), 0); };
-            ok = wait(BAR(B_FF), 0) && wait(BAR(B_0F), 0) && z(B_Z0, 0);
-            tc_fence_after();
-            if (ok) {
-                scores(tS, f0, k0);
-                tc_commit(BAR(B_SF));
-                ok = wait(BAR(B_1F), 0) && z(B_Z1, 0);
+            // (the whole warp, with the same values in every lane: see stream_device.cuh)
+            const int n = uniform(n_tiles), clean = uniform(tail);
+            if (n > 0) {
+                constexpr uint32_t ISS = idesc_bf16_f32(128, 128, false);
+                constexpr uint32_t ITS = idesc_bf16_f32(128, D, true);
+                constexpr uint32_t STEP = LY::TILE >> 4;
+                const uint32_t leader = elect_one();
+                const Desc f0 = make_desc(sdesc_sw128(sbase + LY::OFF_F, 16, 1024));
+                const Desc f1 = make_desc(sdesc_sw128(sbase + LY::OFF_F + LY::TILE, 16, 1024));
+                const Desc k0 = make_desc(sdesc_sw128(sbase + LY::OFF_L0, 16, 1024));  // as K-major operands
+                const Desc k1 = make_desc(sdesc_sw128(sbase + LY::OFF_L1, 16, 1024));
+                const Desc m0 = make_desc(sdesc_sw128(sbase + LY::OFF_L0, 128 * 128, 1024));  // as MN-major operands
+                const Desc m1 = make_desc(sdesc_sw128(sbase + LY::OFF_L1, 128 * 128, 1024));
+                auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(BAR(bar), parity)) != 0; };
+                auto cleaned = [&](int bar, int j) { return !clean || j + 1 < n || wait_all(bar, 0); };
+                bool go = wait_all(B_FF, 0) && wait_all(B_0F, 0) && cleaned(B_Z0, 0);
                 tc_fence_after();
-                if (ok) {
-                    scores(tP, f1, k1);
-                    tc_commit(BAR(B_DPF));
-                }
-            }
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const bool more = j + 1 < n_tiles;
-                const int s = j & 1, s2 = s ^ 1, ph2 = ((j + 1) >> 1) & 1;
-                if (!(ok = wait(BAR(B_PF), j & 1))) break;
-                tc_fence_after();
-                mma8_ts_halves<2048 / 16>(tmem + tA1, tmem + tS, (KEYS ? m1 : m0) + s * STAGE, ITS, j > 0 ? 1u : 0u);
-                tc_commit(BAR(B_1E + s));
-                if (more) {
-                    if (!(ok = wait(BAR(B_0F + s2), ph2) && z(B_Z0, j + 1))) break;
+                if (go) {
+                    mma_rows<D>(leader, tS, f0, k0, ISS);
+                    commit(leader, BAR(B_SF));
+                    go = wait_all(B_1F, 0) && cleaned(B_Z1, 0);
                     tc_fence_after();
-                    scores(tS, f0, k0 + s2 * STAGE);
-                    tc_commit(BAR(B_SF));
+                    if (go) {
+                        mma_rows<D>(leader, tP, f1, k1, ISS);
+                        commit(leader, BAR(B_DPF));
+                    }
                 }
-                if (!(ok = wait(BAR(B_DF), j & 1))) break;
-                tc_fence_after();
-                mma8_ts_halves<2048 / 16>(tmem + tA2, tmem + tP, m0 + s * STAGE, ITS, j > 0 ? 1u : 0u);
-                tc_commit(BAR(B_0E + s));
-                if (more) {
-                    if (!(ok = wait(BAR(B_1F + s2), ph2) && z(B_Z1, j + 1))) break;
+                for (int j = 0; j < n && go; ++j) {
+                    const bool more = j + 1 < n;
+                    const int s = j & 1, s2 = s ^ 1, ph2 = ((j + 1) >> 1) & 1;
+                    const Desc x1 = KEYS ? m1 : m0;
+                    if (!(go = wait_all(B_PF, j & 1))) break;
                     tc_fence_after();
-                    scores(tP, f1, k1 + s2 * STAGE);
-                    tc_commit(BAR(B_DPF));
+                    mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, j > 0 ? 1u : 0u);
+                    commit(leader, BAR(B_1E + s));
+                    if (more) {
+                        if (!(go = wait_all(B_0F + s2, ph2) && cleaned(B_Z0, j + 1))) break;
+                        tc_fence_after();
+                        mma_rows<D>(leader, tS, f0, Desc{k0.lo + s2 * STEP, k0.hi}, ISS);
+                        commit(leader, BAR(B_SF));
+                    }
+                    if (!(go = wait_all(B_DF, j & 1))) break;
+                    tc_fence_after();
+                    mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, j > 0 ? 1u : 0u);
+                    commit(leader, BAR(B_0E + s));
+                    if (more) {
+                        if (!(go = wait_all(B_1F + s2, ph2) && cleaned(B_Z1, j + 1))) break;
+                        tc_fence_after();
+                        mma_rows<D>(leader, tP, f1, Desc{k1.lo + s2 * STEP, k1.hi}, ISS);
+                        commit(leader, BAR(B_DPF));
+                    }
                 }
+                commit(leader, BAR(B_AF));
+                wait(BAR(B_AF), 0);
             }
-            tc_commit(BAR(B_AF));
-            wait(BAR(B_AF), 0);
         } else if (warp == 8 && n_tiles > 0) {
           if (lane == 0) {
             // ------------------------------------------------ TMA producer
