@@ -58,8 +58,9 @@ struct Split {  // threads and registers: bf16 keys launch with 168 each, 8-bit 
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kConvK = 128, kConvV = 96;  // converting threads
 
-template <int D, bool C8>
+template <int D, int GROUP>
 struct Layout {
+    static constexpr bool C8 = GROUP != 0;
     static constexpr int HALVES = D / 64;  // 128-byte column halves of a row
     static constexpr uint32_t TILE = HALVES * 128 * 128;
     static constexpr uint32_t OFF_Q = 0;
@@ -69,7 +70,7 @@ struct Layout {
     static constexpr uint32_t OFF_BAR = OFF_GRP + (C8 ? 4 * 8 * 16 : 0);
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // 1024-byte alignment slack
 };
-static_assert(Layout<128, true>::SMEM <= 232448, "shared memory");
+static_assert(Layout<128, 16>::SMEM <= 232448, "shared memory");
 
 enum {
     B_KF = 0,     // [NS] K stage filled
@@ -106,6 +107,33 @@ struct WinParams {
     OpErr *err;
 };
 
+// 2^x of two values on the FMA pipe: the special-function unit does 16 results
+// per cycle and SM, 2,048 cycles for the exponentials of a pair of 128 x 128 tiles,
+// as long as its products take.  Every kPolyEvery-th pair goes this way.  x = n + f
+// with n = round(x), |f| <= 1/2 (Cody and Waite), n read from the low mantissa bits
+// of x + 1.5 * 2^23; 2^f by a quartic fitted here for least maximum relative error
+// (2.7e-6, mean below 1e-8); 2^n added to the exponent field.  x is clamped at -126:
+// a masked column (-inf) gives 2^-126, which nothing notices.
+constexpr int kPolyEvery = 4;
+constexpr float kExp2C0 = 0.99999922514f, kExp2C1 = 0.69312173128f, kExp2C2 = 0.24024765193f, kExp2C3 = 0.05591819808f,
+                kExp2C4 = 0.00956970546f;
+__device__ __forceinline__ void exp2_fma(uint64_t x2, float &p0, float &p1) {
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+    f2_unpack(x2, p0, p1);
+    const uint64_t x = f2_pack(fmaxf(p0, -126.f), fmaxf(p1, -126.f));
+    const uint64_t t = f2_add(x, f2_pack(kMagic, kMagic));
+    const uint64_t f = f2_sub(x, f2_sub(t, f2_pack(kMagic, kMagic)));
+    uint64_t q = f2_fma(f2_pack(kExp2C4, kExp2C4), f, f2_pack(kExp2C3, kExp2C3));
+    q = f2_fma(q, f, f2_pack(kExp2C2, kExp2C2));
+    q = f2_fma(q, f, f2_pack(kExp2C1, kExp2C1));
+    q = f2_fma(q, f, f2_pack(kExp2C0, kExp2C0));
+    float q0, q1, t0, t1;
+    f2_unpack(q, q0, q1);
+    f2_unpack(t, t0, t1);
+    p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+    p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
+
 __device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 __device__ __forceinline__ uint4 load_codes(const uint8_t *src) {
@@ -114,10 +142,13 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *src) {
     return w;
 }
 
-template <int D, bool C8>
-__global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
+// GROUP: 0 over bf16 keys; over the cache the number of consecutive keys that share
+// their scales, 32 (pages of 32 tokens or more) or 16.
+template <int D, int GROUP>
+__global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
                                                             const __grid_constant__ WinParams p) {
-    using LY = Layout<D, C8>;
+    constexpr bool C8 = GROUP != 0;
+    using LY = Layout<D, GROUP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(sm);
@@ -474,7 +505,8 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                         }
                     }
                 };
-                // row maximum: eight independent ones, over the cache those of the groups of 16 keys
+                // row maximum: eight independent ones, over the cache those of the groups
+                constexpr int NG = C8 ? BN / GROUP : 1;  // groups of a tile
                 float pm[8];
 #pragma unroll
                 for (int a = 0; a < 8; ++a) pm[a] = -INFINITY;
@@ -485,16 +517,20 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                     for (int c = c0; c < c0 + KEEP; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const int a = C8 ? 2 * c + (e >> 4) : (e >> 1) & 7;
+                            const int a = !C8 ? (e >> 1) & 7 : 2 * c + (GROUP == 16 ? e >> 4 : (e >> 1) & 1);
                             pm[a] = fmax3(pm[a], __uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1]));
                         }
                 }
-                const float4 *grp = grp_s + (j & 3) * 8;
+                const float4 *grp = grp_s + (j & 3) * 8;  // of group a: grp[a * GROUP / 16]
                 if (C8) {
 #pragma unroll
-                    for (int a = 0; a < 8; ++a) pm[a] = fmaf(pm[a], sl2 * grp[a].x, grp[a].y);
+                    for (int a = 0; a < NG; ++a) {
+                        const float4 f = grp[a * GROUP / 16];
+                        pm[a] = fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), sl2 * f.x, f.y);
+                    }
                 }
-                const float tmax = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+                const float tmax = NG == 4 ? fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3]))
+                                           : fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
                 const float m_new = fmaxf(m_run, C8 ? tmax : tmax * sl2);
                 // The rescale touches TMEM with warp-collective loads and stores, so
                 // the whole warp moves when one live row's maximum grew by more than 2^8.
@@ -530,18 +566,22 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                         const int c = half * 2 + cc;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            if (C8 && e % 16 == 0) {
+                            if (C8 && e % (C8 ? GROUP : 32) == 0) {
                                 const float4 f = grp[2 * c + e / 16];
                                 const float k = sl2 * f.x, n = f.y - m_use;
                                 sl2x2 = f2_pack(k, k), negm2 = f2_pack(n, n);
                             }
                             const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1])), sl2x2, negm2);
-                            float x0, x1;
-                            f2_unpack(x2, x0, x1);
-                            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                            float p0, p1;
+                            if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
+                                exp2_fma(x2, p0, p1);
+                            } else {
+                                f2_unpack(x2, p0, p1);
+                                p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+                            }
                             ps2[(e >> 1) & 3] = f2_add(ps2[(e >> 1) & 3], f2_pack(p0, p1));
                             pk[cc * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
-                            if (C8 && e % 16 == 14) {
+                            if (C8 && e % (C8 ? GROUP : 32) == (C8 ? GROUP : 32) - 2) {
                                 float a0, a1;
                                 f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
                                 l_tile = fmaf(a0 + a1, grp[2 * c + e / 16].z, l_tile);
@@ -564,7 +604,7 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         }
-        const bool some = active && live && l_run > 0.f;
+        const bool some = active && live && m_run > -INFINITY;
         const float il = some ? 1.f / l_run : 0.f;
         const int64_t orow = ((int64_t)b * p.Hq + hk * p.G + g) * p.Lq + i;
         if (ok && mine) {
@@ -724,10 +764,15 @@ cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s) {
         AC_NOTE_LAUNCH();
         return cudaGetLastError();
     };
+    const int group = !a.k8 ? 0 : a.T == 16 ? 16 : 32;
     if (a.d == 128)
-        e = a.k8 ? go(k_window_attn<128, true>, Layout<128, true>::SMEM) : go(k_window_attn<128, false>, Layout<128, false>::SMEM);
+        e = group == 0    ? go(k_window_attn<128, 0>, Layout<128, 0>::SMEM)
+            : group == 16 ? go(k_window_attn<128, 16>, Layout<128, 16>::SMEM)
+                          : go(k_window_attn<128, 32>, Layout<128, 32>::SMEM);
     else
-        e = a.k8 ? go(k_window_attn<64, true>, Layout<64, true>::SMEM) : go(k_window_attn<64, false>, Layout<64, false>::SMEM);
+        e = group == 0    ? go(k_window_attn<64, 0>, Layout<64, 0>::SMEM)
+            : group == 16 ? go(k_window_attn<64, 16>, Layout<64, 16>::SMEM)
+                          : go(k_window_attn<64, 32>, Layout<64, 32>::SMEM);
     if (e != cudaSuccess || pl.nsplit == 1) return e;
     return launch_combine(p.part_o, p.part_lse, a, pl.nsplit, s);
 }
