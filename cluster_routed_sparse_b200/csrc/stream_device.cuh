@@ -104,13 +104,15 @@ __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, Desc a, De
         mma_ss(leader, d, Desc{a.lo + at, a.hi}, Desc{b.lo + at, b.hi}, idesc, k > 0 ? 1u : 0u);
     }
 }
-// A: 128 x 128 16-bit values in tensor memory, 32 columns for each 64 of K, A_STEP columns apart;
-// B: 128 rows (K) in shared memory, MN-major.
+// Half h (64 of K) of A: 128 x 128 16-bit values in tensor memory, 32 columns for each half, A_STEP
+// columns apart; B: 128 rows (K) in shared memory, MN-major.
 template <int A_STEP>
-__device__ __forceinline__ void mma_weights(uint32_t leader, uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_weights(uint32_t leader, uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t accumulate,
+                                            int h) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        mma_ts(leader, d, a + (k / 4) * A_STEP + (k % 4) * 8, Desc{b.lo + k * (2048 >> 4), b.hi}, idesc, k > 0 ? 1u : accumulate);
+    for (int k = 0; k < 4; ++k)
+        mma_ts(leader, d, a + h * A_STEP + k * 8, Desc{b.lo + (4 * h + k) * (2048 >> 4), b.hi}, idesc,
+               k > 0 || h > 0 ? 1u : accumulate);
 }
 
 // ------------------------------------------------------------------ e4m3

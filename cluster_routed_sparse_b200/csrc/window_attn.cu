@@ -79,12 +79,12 @@ enum {
     B_VE = 6,     // [NS] V stage free (MMA commit after both PV products)
     B_QF = 8,     // query tiles filled
     B_SF = 9,     // [2] S_i written (MMA commit)
-    B_PF = 11,    // [2] P_i written (+ O_i rescaled) by the 128 softmax threads
-    B_OF = 13,    // [2] last PV_i complete (MMA commit)
-    B_DONE = 15,  // every MMA complete
-    B_VZ = 16,    // V rows behind the sequence zeroed (bf16 keys)
-    B_QC = 17,    // query tiles converted to fp16 (8-bit keys)
-    NBAR = 18
+    B_PF = 11,    // [2][2] half of P_i written (+ O_i rescaled) by the four softmax warps
+    B_OF = 15,    // [2] last PV_i complete (MMA commit)
+    B_DONE = 17,  // every MMA complete
+    B_VZ = 18,    // V rows behind the sequence zeroed (bf16 keys)
+    B_QC = 19,    // query tiles converted to fp16 (8-bit keys)
+    NBAR = 20
 };
 
 struct WinMaps {
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(BAR(B_SF + i), 1);
-            mbar_init(BAR(B_PF + i), BM);
+            mbar_init(BAR(B_PF + 2 * i), 4);
+            mbar_init(BAR(B_PF + 2 * i + 1), 4);
             mbar_init(BAR(B_OF + i), 1);
         }
         mbar_init(BAR(B_QF), 1);
@@ -252,8 +253,9 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     mma_rows<D>(leader, i * BN, Desc{dq0.lo + i * STEP, dq0.hi}, Desc{dk0.lo + (j % NS) * STEP, dk0.hi}, IQK);
                     commit(leader, BAR(B_SF + i));
                 };
-                auto issue_pv = [&](int i, int j) {
-                    mma_weights<32>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV, j > 0 ? 1u : 0u);
+                // the products of half h of P_i(j), that is of 64 keys
+                auto issue_pv = [&](int i, int j, int h) {
+                    mma_weights<32>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV, j > 0 ? 1u : 0u, h);
                 };
                 bool go = wait_all(C8 ? B_QC : B_QF, 0) && wait_all(B_KF, 0);
                 tc_fence_after();
@@ -264,24 +266,21 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 }
                 for (int j = 0; j < n && go; ++j) {
                     const bool more = j + 1 < n;
-                    if (!(go = wait_all(B_PF, j & 1) && wait_all(B_VF + j % NS, (j / NS) & 1) &&
-                               (!clean || more || wait_all(B_VZ, 0))))
+                    // V and the next K are there long before P
+                    if (!(go = wait_all(B_VF + j % NS, (j / NS) & 1) && (!clean || more || wait_all(B_VZ, 0)) &&
+                               (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
                         break;
-                    tc_fence_after();
-                    issue_pv(0, j);
-                    if (!more) commit(leader, BAR(B_OF));
-                    if (more) {
-                        if (!(go = wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))) break;
-                        tc_fence_after();
-                        issue_s(0, j + 1);
+                    for (int i = 0; i < (two ? 2 : 1); ++i) {
+                        for (int h = 0; h < 2 && go; ++h) {
+                            if (!(go = wait_all(B_PF + 2 * i + h, j & 1))) break;
+                            tc_fence_after();
+                            issue_pv(i, j, h);
+                        }
+                        if (!go) break;
+                        if (more) issue_s(i, j + 1);
+                        else commit(leader, BAR(B_OF + i));
                     }
-                    if (two) {
-                        if (!(go = wait_all(B_PF + 1, j & 1))) break;
-                        tc_fence_after();
-                        issue_pv(1, j);
-                        if (!more) commit(leader, BAR(B_OF + 1));
-                        if (more) issue_s(1, j + 1);
-                    }
+                    if (!go) break;
                     if (more) commit(leader, BAR(B_KE + (j + 1) % NS));
                     commit(leader, BAR(B_VE + j % NS));
                 }
@@ -591,14 +590,15 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                         }
                     }
                     tmem_st32(tS + half * 32, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(B_PF + 2 * wg + half));
                 }
                 float ps[8];
 #pragma unroll
                 for (int a = 0; a < 4; ++a) f2_unpack(ps2[a], ps[2 * a], ps[2 * a + 1]);
-                tmem_st_wait();
                 l_run += C8 ? l_tile : ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-                tc_fence_before();
-                mbar_arrive(BAR(B_PF + wg));
             }
             if (ok && !__all_sync(0xFFFFFFFFu, wait(BAR(B_OF + wg), 0))) ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
