@@ -124,11 +124,11 @@ extern "C" ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view
         for (int k = 0; k < pairs[i]; ++k) {
             const double f = freq[a.P];
             if (!std::isfinite(f)) return refuse("ac_rope_axes: frequencies must be finite");
-            const long double two_pi = 6.283185307179586476925286766559L;
-            long double t = fmodl((long double)f / two_pi, 1.0L);
-            if (t < 0) t += 1.0L;
-            const long double scaled = roundl(t * 18446744073709551616.0L);
-            a.turns[a.P] = scaled >= 18446744073709551616.0L ? 0 : (uint64_t)scaled;
+            // turns per step modulo 1, in units of 2^-64, to the nearest
+            long double t = (long double)f * 0.159154943091895335768883763372514362L;
+            if (t >= 1.0L || t <= -1.0L) t = fmodl(t, 1.0L);
+            const uint64_t units = (uint64_t)((t < 0 ? -t : t) * 18446744073709551615.0L + 0.5L);
+            a.turns[a.P] = t < 0 ? 0 - units : units;
             a.axis[a.P] = (uint8_t)i;
             ++a.P;
         }

@@ -29,26 +29,38 @@ _ROPE_DTYPES = {torch.bfloat16: _lib.AC_DTYPE_BF16, torch.float16: _lib.AC_DTYPE
 _NO_VIEW = ACView(None, 0, 0, 0)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device, fn, *args):
     """fn(*args, stream) with `device` current."""
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
     if device.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream().cuda_stream))
+        status = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            check(fn(*args, torch.cuda.current_stream().cuda_stream))
+            status = fn(*args, _raw_stream(device.index))
+    if status:
+        check(status)
 
 
-def _view(t, name, device, shape=None, dtype=torch.bfloat16):
-    if t.dtype != dtype:
+def _shape(t, name):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, H, L, d], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _view(t, name, device, shape, dtype=torch.bfloat16):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be [B, H, L, d]" + (f" = {shape}" if shape else "") + f", got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [B, H, L, d] = {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     b, h, row, e = t.stride()
-    if e != 1 and t.shape[3] > 1:
+    if e != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return ACView(t.data_ptr(), b, h, row)
 
@@ -57,8 +69,8 @@ def _ints(t, name, device, shape):
     """Pointer of a contiguous int32 tensor, or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
@@ -93,55 +105,58 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
     the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
     fp32.  Returns (q, k) rotated, or q alone when k is None."""
-    dtype = _ROPE_DTYPES.get(q.dtype)
+    dt = q.dtype
+    dtype = _ROPE_DTYPES.get(dt)
     if dtype is None:
         raise TypeError("q must be bf16, fp16 or fp32")
     dev = q.device
-    vq = _view(q, "q", dev, None, q.dtype)
-    B, Hq, L, d = q.shape
+    shape = _shape(q, "q")
+    vq = _view(q, "q", dev, shape, dt)
+    B, Hq, L, d = shape
     pairs = tuple(pairs)
+    axes = len(pairs)
     if freqs is not None:
         freq, npairs = _axes_given(pairs, tuple(freqs))
     else:
-        freq, npairs = _axes(pairs, theta if not isinstance(theta, (list, tuple)) else tuple(theta))
-    axes = len(pairs)
+        freq, npairs = _axes(pairs, tuple(theta) if isinstance(theta, (list, tuple)) else theta)
     if positions.dim() == 3:
         pos, pos_b = _ints(positions, "positions", dev, (B, L, axes)), L * axes
     else:
         pos, pos_b = _ints(positions, "positions", dev, (L, axes)), 0
-    Hk = 0
-    vk = vko = _NO_VIEW
-    oq, ok = out if out is not None else (None, None)
+    oq, ok = (None, None) if out is None else out
     if oq is None:
-        oq = torch.empty((B, Hq, L, d), dtype=q.dtype, device=dev)
-    vqo = _view(oq, "out[0]", dev, (B, Hq, L, d), q.dtype)
+        oq = q.new_empty(shape)
+    vqo = _view(oq, "out[0]", dev, shape, dt)
+    Hk, vk, vko = 0, _NO_VIEW, _NO_VIEW
     if k is not None:
-        Hk = k.shape[1] if k.dim() == 4 else 0
-        vk = _view(k, "k", dev, (B, Hk, L, d), q.dtype)
+        Hk = _shape(k, "k")[1]
+        kshape = (B, Hk, L, d)
+        vk = _view(k, "k", dev, kshape, dt)
         if ok is None:
-            ok = torch.empty((B, Hk, L, d), dtype=q.dtype, device=dev)
-        vko = _view(ok, "out[1]", dev, (B, Hk, L, d), q.dtype)
+            ok = q.new_empty(kshape)
+        vko = _view(ok, "out[1]", dev, kshape, dt)
     _on(dev, _lib.load().ac_rope_axes, dtype, vq, vqo, Hq, vk, vko, Hk, B, L, d, pos, pos_b, freq, npairs, axes,
-        int(interleaved), int(inverse))
+        1 if interleaved else 0, 1 if inverse else 0)
     return oq if k is None else (oq, ok)
 
 
 # ---------------------------------------------------------------- window attention
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=1024)
 def _window(left, right, sinks, block, scale):
     return ACWindow(left, right, sinks, block, scale)
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
 @functools.lru_cache(maxsize=1024)
-def _window_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block):
+def _window_plan(left, right, sinks, block, scale, *sizes):
+    """The window and the bytes of workspace of window_attn at these sizes."""
     n = ctypes.c_int64(0)
-    check(_lib.load().ac_window_attn_workspace(B, Hq, Hk, Lq, Lk, d, _window(left, right, sinks, block, 0.0),
-                                               ctypes.byref(n)))
-    return n.value
+    w = _window(left, right, sinks, block, scale)
+    check(_lib.load().ac_window_attn_workspace(*sizes, w, ctypes.byref(n)))
+    return w, n.value
+
+
+def _workspace(nbytes, like):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _ptr(t):
@@ -156,20 +171,27 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
     ac_window says exactly which keys a query sees).  q_lens, k_lens: int32 [B]
     lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32."""
     dev = q.device
-    vq = _view(q, "q", dev)
-    B, Hq, Lq, d = q.shape
-    Hk, Lk = (k.shape[1], k.shape[2]) if k.dim() == 4 else (0, 0)
-    vk, vv = _view(k, "k", dev, (B, Hk, Lk, d)), _view(v, "v", dev, (B, Hk, Lk, d))
+    shape = _shape(q, "q")
+    B, Hq, Lq, d = shape
+    _, Hk, Lk, _ = _shape(k, "k")
+    kshape = (B, Hk, Lk, d)
+    vq, vk, vv = _view(q, "q", dev, shape), _view(k, "k", dev, kshape), _view(v, "v", dev, kshape)
     if out is None:
-        out = torch.empty((B, Hq, Lq, d), dtype=torch.bfloat16, device=dev)
-    vo = _view(out, "out", dev, (B, Hq, Lq, d))
-    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev) if return_lse else None
-    n = _window_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block)
-    ws = _workspace(n, dev)
+        out = q.new_empty(shape)
+    vo = _view(out, "out", dev, shape)
+    lse = q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
+    w, n = _window_plan(left, right, sinks, block, scale, B, Hq, Hk, Lq, Lk, d)
+    ws = _workspace(n, q)
     _on(dev, _lib.load().ac_window_attn, vq, vk, vv, vo, _ptr(lse), B, Hq, Hk, Lq, Lk, d,
-        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)),
-        _window(left, right, sinks, block, scale), _ptr(ws), n)
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n)
     return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block):
+    n = ctypes.c_int64(0)
+    check(_lib.load().ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, ctypes.byref(n)))
+    return n.value
 
 
 def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1,
@@ -178,25 +200,21 @@ def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int =
     d_out, the gradient of o, and the o and lse that it returned
     (ac_window_attn_backward).  out: (dq, dk, dv) to write into."""
     dev = q.device
-    vq = _view(q, "q", dev)
-    B, Hq, Lq, d = q.shape
-    Hk, Lk = (k.shape[1], k.shape[2]) if k.dim() == 4 else (0, 0)
-    qs, ks = (B, Hq, Lq, d), (B, Hk, Lk, d)
-    vk, vv = _view(k, "k", dev, ks), _view(v, "v", dev, ks)
+    qs = _shape(q, "q")
+    B, Hq, Lq, d = qs
+    _, Hk, Lk, _ = _shape(k, "k")
+    ks = (B, Hk, Lk, d)
+    vq, vk, vv = _view(q, "q", dev, qs), _view(k, "k", dev, ks), _view(v, "v", dev, ks)
     vo, vg = _view(o, "o", dev, qs), _view(d_out, "d_out", dev, qs)
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Lq) or not lse.is_contiguous() or lse.device != dev:
+    if lse.dtype is not torch.float32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be a contiguous fp32 tensor {(B, Hq, Lq)} on {dev}")
-    if out is None:
-        out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in (qs, ks, ks))
-    dq, dk, dv = out
-    n = ctypes.c_int64(0)
-    lib = _lib.load()
-    check(lib.ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, ctypes.byref(n)))
-    ws = _workspace(n.value, dev)
-    _on(dev, lib.ac_window_attn_backward, vg, vq, vk, vv, vo, lse.data_ptr(), _view(dq, "dq", dev, qs),
+    dq, dk, dv = (q.new_empty(qs), q.new_empty(ks), q.new_empty(ks)) if out is None else out
+    n = _backward_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block)
+    ws = _workspace(n, q)
+    _on(dev, _lib.load().ac_window_attn_backward, vg, vq, vk, vv, vo, lse.data_ptr(), _view(dq, "dq", dev, qs),
         _view(dk, "dk", dev, ks), _view(dv, "dv", dev, ks), B, Hq, Hk, Lq, Lk, d,
         _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)),
-        _window(left, right, sinks, block, scale), _ptr(ws), n.value)
+        _window(left, right, sinks, block, scale), _ptr(ws), n)
     return dq, dk, dv
 
 
@@ -219,15 +237,19 @@ class Cache8(NamedTuple):
 
 
 def _cache(c, dev):
-    pages, heads, T, d = c.k.shape
-    for t, n in ((c.k, "k"), (c.v, "v")):
-        if t.dtype != torch.float8_e4m3fn or tuple(t.shape) != (pages, heads, T, d) or not t.is_contiguous() \
-                or t.device != dev:
-            raise ValueError(f"cache.{n} must be a contiguous float8_e4m3fn tensor [pages, heads, page_tokens, d] on {dev}")
-    for t, n in ((c.k_scale, "k_scale"), (c.v_scale, "v_scale")):
-        if t.dtype != torch.float32 or tuple(t.shape) != (pages, heads) or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"cache.{n} must be a contiguous fp32 tensor [pages, heads] on {dev}")
-    return ACCache8(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), pages, heads, T, d)
+    k, v, ks, vs = c
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("cache.k must be [pages, heads, page_tokens, d]")
+    pages, heads, T, d = shape
+    for t in (k, v):
+        if t.dtype is not torch.float8_e4m3fn or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError("cache.k and cache.v must be contiguous float8_e4m3fn tensors [pages, heads, page_tokens, d] "
+                             f"on {dev}")
+    for t in (ks, vs):
+        if t.dtype is not torch.float32 or t.shape != (pages, heads) or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"cache.k_scale and cache.v_scale must be contiguous fp32 tensors [pages, heads] on {dev}")
+    return ACCache8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, T, d)
 
 
 def cache8_append(k, v, cache: Cache8, page_table, start, counts=None):
@@ -235,17 +257,27 @@ def cache8_append(k, v, cache: Cache8, page_table, start, counts=None):
     first start[b] tokens into the cache (ac_cache8_append).  page_table: int32
     [B, max_pages]; start, counts: int32 [B] (counts: how many of the n are real)."""
     dev = k.device
-    vk = _view(k, "k", dev)
-    B, H, n, d = k.shape
-    vv = _view(v, "v", dev, (B, H, n, d))
+    shape = _shape(k, "k")
+    B, H, n, d = shape
+    vk, vv = _view(k, "k", dev, shape), _view(v, "v", dev, shape)
     c = _cache(cache, dev)
-    if (H, d) != (c.heads, c.d):
+    if H != c.heads or d != c.d:
         raise ValueError(f"k has {H} heads of {d}, the cache {c.heads} of {c.d}")
     if start is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages] and start [B]")
-    _on(dev, _lib.load().ac_cache8_append, c, vk, vv, B, n,
-        _ints(page_table, "page_table", dev, (B, page_table.shape[1])), page_table.shape[1],
+    per = page_table.shape[1]
+    _on(dev, _lib.load().ac_cache8_append, c, vk, vv, B, n, _ints(page_table, "page_table", dev, (B, per)), per,
         _ints(start, "start", dev, (B,)), _ints(counts, "counts", dev, (B,)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_plan(left, right, sinks, block, scale, B, Hq, Lq, per, heads, T, d):
+    """The window and the bytes of workspace of cache8_attn at these sizes."""
+    n = ctypes.c_int64(0)
+    w = _window(left, right, sinks, block, scale)
+    sizes = ACCache8(256, 256, 256, 256, 0, heads, T, d)  # (addresses that are never read)
+    check(_lib.load().ac_cache8_attn_workspace(sizes, B, Hq, Lq, per, w, ctypes.byref(n)))
+    return w, n.value
 
 
 def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1,
@@ -253,24 +285,23 @@ def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: 
     """window_attn of q [B, Hq, Lq, d] over the first k_lens[b] cached tokens of each
     sequence (ac_cache8_attn)."""
     dev = q.device
-    vq = _view(q, "q", dev)
-    B, Hq, Lq, d = q.shape
+    shape = _shape(q, "q")
+    vq = _view(q, "q", dev, shape)
+    B, Hq, Lq, d = shape
     c = _cache(cache, dev)
     if d != c.d:
         raise ValueError(f"q has heads of {d}, the cache of {c.d}")
     if k_lens is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages] and k_lens [B]")
     if out is None:
-        out = torch.empty((B, Hq, Lq, d), dtype=torch.bfloat16, device=dev)
-    vo = _view(out, "out", dev, (B, Hq, Lq, d))
-    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev) if return_lse else None
-    lib, w = _lib.load(), _window(left, right, sinks, block, scale)
-    n = ctypes.c_int64(0)
-    check(lib.ac_cache8_attn_workspace(c, B, Hq, Lq, page_table.shape[1], w, ctypes.byref(n)))
-    ws = _workspace(n.value, dev)
-    _on(dev, lib.ac_cache8_attn, c, vq, vo, _ptr(lse), B, Hq, Lq,
-        _ints(page_table, "page_table", dev, (B, page_table.shape[1])), page_table.shape[1],
-        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n.value)
+        out = q.new_empty(shape)
+    vo = _view(out, "out", dev, shape)
+    lse = q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
+    per = page_table.shape[1]
+    w, n = _cache_plan(left, right, sinks, block, scale, B, Hq, Lq, per, c.heads, c.page_tokens, d)
+    ws = _workspace(n, q)
+    _on(dev, _lib.load().ac_cache8_attn, c, vq, vo, _ptr(lse), B, Hq, Lq, _ints(page_table, "page_table", dev, (B, per)), per,
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n)
     return (out, lse) if return_lse else out
 
 
