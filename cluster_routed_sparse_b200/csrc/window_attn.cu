@@ -107,33 +107,6 @@ struct WinParams {
     OpErr *err;
 };
 
-// 2^x of two values on the FMA pipe: the special-function unit does 16 results
-// per cycle and SM, 2,048 cycles for the exponentials of a pair of 128 x 128 tiles,
-// as long as its products take.  Every kPolyEvery-th pair goes this way.  x = n + f
-// with n = round(x), |f| <= 1/2 (Cody and Waite), n read from the low mantissa bits
-// of x + 1.5 * 2^23; 2^f by a quartic fitted here for least maximum relative error
-// (2.7e-6, mean below 1e-8); 2^n added to the exponent field.  x is clamped at -126:
-// a masked column (-inf) gives 2^-126, which nothing notices.
-constexpr int kPolyEvery = 4;
-constexpr float kExp2C0 = 0.99999922514f, kExp2C1 = 0.69312173128f, kExp2C2 = 0.24024765193f, kExp2C3 = 0.05591819808f,
-                kExp2C4 = 0.00956970546f;
-__device__ __forceinline__ void exp2_fma(uint64_t x2, float &p0, float &p1) {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-    f2_unpack(x2, p0, p1);
-    const uint64_t x = f2_pack(fmaxf(p0, -126.f), fmaxf(p1, -126.f));
-    const uint64_t t = f2_add(x, f2_pack(kMagic, kMagic));
-    const uint64_t f = f2_sub(x, f2_sub(t, f2_pack(kMagic, kMagic)));
-    uint64_t q = f2_fma(f2_pack(kExp2C4, kExp2C4), f, f2_pack(kExp2C3, kExp2C3));
-    q = f2_fma(q, f, f2_pack(kExp2C2, kExp2C2));
-    q = f2_fma(q, f, f2_pack(kExp2C1, kExp2C1));
-    q = f2_fma(q, f, f2_pack(kExp2C0, kExp2C0));
-    float q0, q1, t0, t1;
-    f2_unpack(q, q0, q1);
-    f2_unpack(t, t0, t1);
-    p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-    p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
-}
-
 __device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 __device__ __forceinline__ uint4 load_codes(const uint8_t *src) {
@@ -354,8 +327,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     if (!IS_V) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
                     return -1;
                 };
-                float ks = 1.f, vs = 1.f;  // of this lane's page
-                auto scales_of = [&](int page) {
+                auto scales_of = [&](int page, float &ks, float &vs) {
                     ks = vs = 1.f;
                     if (page < 0) return;
                     if (!IS_V) ks = __ldg(p.ks + (int64_t)page * p.Hk + hk);
@@ -372,10 +344,13 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                         if (pg >= 0 && r < rows) w[k] = load_codes(codes + pg * page_bytes + (r & (p.T - 1)) * D + (c % CPR) * 16);
                     }
                 };
+                // The codes of tile j + 1 are loaded one tile ahead, its scales two, its page number three.
                 int page = page_of(0), next = page_of(1);
-                scales_of(page);
-                if (IS_V && vs < kMinScale) page = -1;
-                load(0, page);
+                float ks, vs, ks1, vs1;  // of this lane's page of tile j, and of tile j + 1
+                scales_of(page, ks, vs);
+                load(0, IS_V && vs < kMinScale ? -1 : page);
+                scales_of(next, ks1, vs1);
+                page = next, next = page_of(2);
                 for (int j = 0; j < n_tiles; ++j) {
                     const int s = j % NS;
                     if (!__all_sync(0xFFFFFFFFu, j < NS || wait(BAR((IS_V ? B_VE : B_KE) + s), ((j / NS) - 1) & 1))) {
@@ -406,12 +381,11 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     fence_proxy_async_smem();
                     mbar_arrive(BAR((IS_V ? B_VF : B_KF) + s));
                     if (j + 1 < n_tiles) {
-                        page = next;
-                        next = page_of(j + 2);
-                        scales_of(page);
-                        // (the V page's scale decides whether its codes count: it is waited for here)
-                        if (IS_V && vs < kMinScale) page = -1;
-                        load(j + 1, page);
+                        // (a V page whose scale is below 2^-90 counts as zeros)
+                        load(j + 1, IS_V && vs1 < kMinScale ? -1 : page);
+                        ks = ks1, vs = vs1;
+                        scales_of(next, ks1, vs1);
+                        page = next, next = page_of(j + 3);
                     }
                 }
             };
@@ -473,9 +447,10 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             for (int j = 0; j < n_tiles && ok; ++j) {
                 // Wait outcomes are combined across the warp: the TMEM loads and
                 // stores below are warp-collective, so a warp leaves together.
-                bool got = wait(BAR(B_SF + wg), j & 1);
-                if (C8) got = wait(BAR(B_KF + j % NS), (j / NS) & 1) && got;  // the tile's groups came with K
-                if (!__all_sync(0xFFFFFFFFu, got)) {
+                // (Over the cache S also tells that the tile's groups are there: they were stored
+                // before K was, which S waited for.  A wait for K itself could miss its phase:
+                // K of tile j + 2 may be there already.)
+                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_SF + wg), j & 1))) {
                     ok = false;
                     break;
                 }
@@ -572,12 +547,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                             }
                             const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1])), sl2x2, negm2);
                             float p0, p1;
-                            if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
-                                exp2_fma(x2, p0, p1);
-                            } else {
-                                f2_unpack(x2, p0, p1);
-                                p0 = ex2_approx(p0), p1 = ex2_approx(p1);
-                            }
+                            f2_unpack(x2, p0, p1);
+                            p0 = ex2_approx(p0), p1 = ex2_approx(p1);
                             ps2[(e >> 1) & 3] = f2_add(ps2[(e >> 1) & 3], f2_pack(p0, p1));
                             pk[cc * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
                             if (C8 && e % (C8 ? GROUP : 32) == (C8 ? GROUP : 32) - 2) {
