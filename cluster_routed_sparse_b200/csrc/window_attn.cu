@@ -13,17 +13,21 @@
 // the 128-key tiles that meet any of its rows' and masks columns only in tiles
 // where some row of the warp does not see all of them.
 //
-// Warp roles (three warpgroups; four over 8-bit keys):
+// Warp roles (three warpgroups; five over 8-bit keys):
 //   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t
 //   warp 8           TMA producer (Q; bf16 keys: K and V, and in the last tile it
 //                    zeroes the V rows behind the sequence: 0 x garbage would be NaN)
 //   warp 9           TMEM allocator and tcgen05.mma issuer
-//   8-bit keys: warps 12-15 load the codes of K, warps 8, 10, 11 those of V, into
-//               registers, and store them as fp16 (exact, one conversion for
-//               two codes) in the swizzled layout that the products read.  The
-//               loads of the next tile are in flight while a thread waits for its
-//               stage, and the page numbers and scales of the one after that too.
-// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P overwrites S as bf16.
+//   8-bit keys: warps 12-15 load the codes of K and warps 16-19 those of V into
+//               registers and store them as fp16 (exact, one conversion for two
+//               codes) in the swizzled layout that the products read.  The codes of
+//               the next tile are in flight while a thread waits for its stage, and
+//               the scales and page numbers of the ones after that too.  Each thread
+//               keeps its place within 16 rows, so that a tile costs few address
+//               computations: the issue slots, and the instruction cache, are
+//               shared with the softmax.
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; each half of P overwrites
+// the first half of the scores it came from.
 // Few query tiles: the key tiles are split over several CTAs, whose partial O
 // and log-sum-exp k_combine joins.
 //
@@ -39,8 +43,6 @@
 // else is fp32.
 // Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
 // issued and frees its TMEM.
-#include <type_traits>
-
 #include "stream_device.cuh"
 #include "stream_host.h"
 
@@ -50,13 +52,13 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr int NS = 2;  // K/V stages
 template <bool C8>
-struct Split {  // threads and registers: bf16 keys launch with 168 each, 8-bit keys with 128
-    static constexpr int THREADS = C8 ? 512 : 384;
-    static constexpr uint32_t SOFTMAX = C8 ? 152 : 200, OTHER = C8 ? 104 : 72;
-    static_assert(2 * 128 * SOFTMAX + (THREADS - 256) * OTHER <= THREADS * (C8 ? 128 : 168), "register split exceeds the launch");
+struct Split {  // threads and registers: bf16 keys launch with 168 each, 8-bit keys with 96
+    static constexpr int THREADS = C8 ? 640 : 384;
+    static constexpr uint32_t SOFTMAX = C8 ? 152 : 200, OTHER = C8 ? 48 : 72, CONVERT = 64;
+    static_assert(2 * SOFTMAX + OTHER + (C8 ? 2 * CONVERT : 0) <= THREADS / 128 * (C8 ? 96 : 168), "register split exceeds the launch");
 };
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kConvK = 128, kConvV = 96;  // converting threads
+constexpr int kConverters = 128;  // threads that convert K, and as many V
 
 template <int D, int GROUP>
 struct Layout {
@@ -122,6 +124,9 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                                                             const __grid_constant__ WinParams p) {
     constexpr bool C8 = GROUP != 0;
     using LY = Layout<D, GROUP>;
+    // The half of a tile's keys whose weights come first: over the cache the one that the
+    // search for the maximum has read last.
+    constexpr int FIRST_HALF = C8 ? 1 : 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(sm);
@@ -178,9 +183,9 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(BAR(B_KF + i), C8 ? kConvK : 1);
+            mbar_init(BAR(B_KF + i), C8 ? kConverters : 1);
             mbar_init(BAR(B_KE + i), 1);
-            mbar_init(BAR(B_VF + i), C8 ? kConvV : 1);
+            mbar_init(BAR(B_VF + i), C8 ? kConverters : 1);
             mbar_init(BAR(B_VE + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -205,7 +210,98 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    if (warp >= 8) {
+    if (C8 && warp >= 12) {
+        reg_dealloc<Split<C8>::CONVERT>();
+        if constexpr (C8) {
+            // ------------------------------------------------ 8-bit pages to fp16 tiles
+            const bool is_v = warp >= 16;
+            const int ct = tid & 127, log_t = 31 - __clz(p.T);
+            const int *table = p.table + (int64_t)b * p.max_pages;
+            const float *scale_v = p.vs + hk, *scale_k = p.ks + hk;
+            // A thread converts 16 codes of every 16 RS-th row: row r0 + RS k of a tile, chunk e.
+            constexpr int CPR = D / 16, RS = kConverters / CPR, NCH = BN / RS;
+            const int r0 = ct / CPR, e = ct % CPR;
+            // Lane i < 8: table entry of keys 16 i .. 16 i + 15 of tile j, -1 where this CTA sees none
+            // of them (then the table may hold anything); and the page, -1 when there is none.
+            auto entry_of = [&](int j) -> int {
+                if (lane >= 8 || j >= n_tiles) return -1;
+                const int key = (tile_base(j) + 16 * lane) >> log_t << log_t;
+                if (!((key < hi_c && key + p.T > lo_c) || key < sink_c)) return -1;
+                const int page = __ldg(table + (key >> log_t));
+                return page == -1 ? -2 : page;
+            };
+            auto page_of = [&](int entry) -> int {
+                if (entry >= 0 && entry < p.pages) return entry;
+                if (entry != -1) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
+                return -1;
+            };
+            auto scales_of = [&](int page, float &ks, float &vs) {
+                ks = page >= 0 ? __ldg(scale_k + (int64_t)page * p.Hk) : 1.f;
+                vs = page >= 0 ? __ldg(scale_v + (int64_t)page * p.Hk) : 1.f;
+            };
+            uint4 w[NCH];
+            // Codes of tile j; `page`: of this lane's group of 16 keys.
+            auto load = [&](int j, int page) {
+                const uint8_t *group = nullptr;  // the group's first row
+                if (page >= 0) group = (is_v ? p.v8 : p.k8) + (((int64_t)page * p.Hk + hk) * p.T + (16 * lane & (p.T - 1))) * D;
+                const int rows = kl - tile_base(j);
+#pragma unroll
+                for (int k = 0; k < NCH; ++k) {
+                    const unsigned long long at = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(group), (r0 + RS * k) >> 4);
+                    w[k] = make_uint4(0, 0, 0, 0);
+                    if (at && r0 + RS * k < rows) w[k] = load_codes(reinterpret_cast<const uint8_t *>(at) + (r0 & 15) * D + e * 16);
+                }
+            };
+            // 128-byte rows of a column half, 16-byte pieces swizzled by the row
+            uint8_t *dst = sm + (is_v ? LY::OFF_V : LY::OFF_K) + (e / 4) * BN * 128 + r0 * 128;
+            const int sw0 = (((e % 4) * 2) ^ (r0 & 7)) << 4, sw1 = (((e % 4) * 2 + 1) ^ (r0 & 7)) << 4;
+            if (n_tiles > 0) {
+                // The codes of tile j + 1 are loaded one tile ahead, its scales two, its table entry three:
+                // nothing here waits for a load that was just issued.
+                int entry = entry_of(1), page = page_of(entry_of(0));
+                float ks, vs, ks1, vs1;  // of this lane's page of tile j, and of tile j + 1
+                scales_of(page, ks, vs);
+                load(0, is_v && vs < kMinScale ? -1 : page);
+                page = page_of(entry);
+                scales_of(page, ks1, vs1);
+                entry = entry_of(2);
+                for (int j = 0; j < n_tiles; ++j) {
+                    const int s = j % NS;
+                    if (!__all_sync(0xFFFFFFFFu, j < NS || wait(BAR((is_v ? B_VE : B_KE) + s), ((j / NS) - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    if (!is_v && ct < 8) {
+                        // What the softmax needs of the group: the scale of K, the exponent of the
+                        // scale of V and its inverse.  (The slot's last readers are four tiles back.)
+                        const float ev = fmaxf(__log2f(vs), kMinLogScale);
+                        grp_s[(j & 3) * 8 + ct] = make_float4(ks, ev, ex2_approx(-ev), 0.f);
+                    }
+                    uint8_t *d = dst + s * LY::TILE;
+#pragma unroll
+                    for (int k = 0; k < NCH; ++k) {
+                        *reinterpret_cast<uint4 *>(d + k * RS * 128 + sw0) =
+                            make_uint4(e4m3x2_to_half2(w[k].x & 0xFFFFu), e4m3x2_to_half2(w[k].x >> 16),
+                                       e4m3x2_to_half2(w[k].y & 0xFFFFu), e4m3x2_to_half2(w[k].y >> 16));
+                        *reinterpret_cast<uint4 *>(d + k * RS * 128 + sw1) =
+                            make_uint4(e4m3x2_to_half2(w[k].z & 0xFFFFu), e4m3x2_to_half2(w[k].z >> 16),
+                                       e4m3x2_to_half2(w[k].w & 0xFFFFu), e4m3x2_to_half2(w[k].w >> 16));
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(BAR((is_v ? B_VF : B_KF) + s));
+                    if (j + 1 < n_tiles) {
+                        // (a V page whose scale is below 2^-90 counts as zeros)
+                        load(j + 1, is_v && vs1 < kMinScale ? -1 : page);
+                        ks = ks1, vs = vs1;
+                        page = page_of(entry);
+                        scales_of(page, ks1, vs1);
+                        entry = entry_of(j + 3);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
         reg_dealloc<Split<C8>::OTHER>();
         if (warp == 9) {
             // ------------------------------------------------ MMA issuer
@@ -226,9 +322,10 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     mma_rows<D>(leader, i * BN, Desc{dq0.lo + i * STEP, dq0.hi}, Desc{dk0.lo + (j % NS) * STEP, dk0.hi}, IQK);
                     commit(leader, BAR(B_SF + i));
                 };
-                // the products of half h of P_i(j), that is of 64 keys
+                // the products of 64 keys, half h of P_i(j)
                 auto issue_pv = [&](int i, int j, int h) {
-                    mma_weights<32>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV, j > 0 ? 1u : 0u, h);
+                    mma_weights<64>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV,
+                                    j > 0 || h != FIRST_HALF ? 1u : 0u, h);
                 };
                 bool go = wait_all(C8 ? B_QC : B_QF, 0) && wait_all(B_KF, 0);
                 tc_fence_after();
@@ -237,14 +334,21 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     if (two) issue_s(1, 0);
                     commit(leader, BAR(B_KE));
                 }
+                bool there = false;  // V(j) and K(j + 1) are known to be there
                 for (int j = 0; j < n && go; ++j) {
                     const bool more = j + 1 < n;
-                    // V and the next K are there long before P
-                    if (!(go = wait_all(B_VF + j % NS, (j / NS) & 1) && (!clean || more || wait_all(B_VZ, 0)) &&
-                               (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
+                    if (!there && !(go = wait_all(B_VF + j % NS, (j / NS) & 1) &&
+                                         (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
                         break;
+                    if (clean && !more && !(go = wait_all(B_VZ, 0))) break;
                     for (int i = 0; i < (two ? 2 : 1); ++i) {
-                        for (int h = 0; h < 2 && go; ++h) {
+                        for (int hh = 0; hh < 2 && go; ++hh) {
+                            const int h = hh ^ FIRST_HALF;
+                            // The last half of P is waited for longest: time to ask for what the next
+                            // iteration reads (a wait costs 150 cycles even when it is over).
+                            if (i == (two ? 1 : 0) && hh == 1)
+                                there = more && __all_sync(0xFFFFFFFFu, mbar_test(BAR(B_VF + (j + 1) % NS), ((j + 1) / NS) & 1) &&
+                                                                            (j + 2 >= n || mbar_test(BAR(B_KF + j % NS), ((j + 2) / NS) & 1)));
                             if (!(go = wait_all(B_PF + 2 * i + h, j & 1))) break;
                             tc_fence_after();
                             issue_pv(i, j, h);
@@ -305,96 +409,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 if (lane == 0) mbar_arrive(BAR(B_VZ));
             }
         }
-        if constexpr (C8) {
-            // ------------------------------------------------ 8-bit pages to fp16 tiles
-            __syncwarp();
-            const int *table = p.table + (int64_t)b * p.max_pages;
-            const int log_t = 31 - __clz(p.T);
-            // One kind (K or V) of tile after tile; thread ct of NT.
-            auto convert = [&](auto kind, auto nthreads, int ct) {
-                constexpr bool IS_V = decltype(kind)::value;
-                constexpr int NT = decltype(nthreads)::value, CPR = D / 16, NCH = (BN * CPR + NT - 1) / NT;  // 16-code chunks
-                const uint8_t *codes = (IS_V ? p.v8 : p.k8) + (int64_t)hk * p.T * D;
-                const int64_t page_bytes = (int64_t)p.Hk * p.T * D;
-                // Lane i < 8: page of keys 16 i .. 16 i + 15 of tile j, -1 where this CTA sees none of
-                // them (then the table may hold anything) or the index is out of range.
-                auto page_of = [&](int j) -> int {
-                    if (lane >= 8 || j >= n_tiles) return -1;
-                    const int key = (tile_base(j) + 16 * lane) >> log_t << log_t;
-                    if (!((key < hi_c && key + p.T > lo_c) || key < sink_c)) return -1;
-                    const int page = __ldg(table + (key >> log_t));
-                    if (page >= 0 && page < p.pages) return page;
-                    if (!IS_V) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
-                    return -1;
-                };
-                auto scales_of = [&](int page, float &ks, float &vs) {
-                    ks = vs = 1.f;
-                    if (page < 0) return;
-                    if (!IS_V) ks = __ldg(p.ks + (int64_t)page * p.Hk + hk);
-                    vs = __ldg(p.vs + (int64_t)page * p.Hk + hk);
-                };
-                uint4 w[NCH];
-                auto load = [&](int j, int page) {
-                    const int rows = min(kl - tile_base(j), BN);
-#pragma unroll
-                    for (int k = 0; k < NCH; ++k) {
-                        const int c = ct + NT * k, r = c / CPR;
-                        const int pg = __shfl_sync(0xFFFFFFFFu, page, (r >> 4) & 7);
-                        w[k] = make_uint4(0, 0, 0, 0);
-                        if (pg >= 0 && r < rows) w[k] = load_codes(codes + pg * page_bytes + (r & (p.T - 1)) * D + (c % CPR) * 16);
-                    }
-                };
-                // The codes of tile j + 1 are loaded one tile ahead, its scales two, its page number three.
-                int page = page_of(0), next = page_of(1);
-                float ks, vs, ks1, vs1;  // of this lane's page of tile j, and of tile j + 1
-                scales_of(page, ks, vs);
-                load(0, IS_V && vs < kMinScale ? -1 : page);
-                scales_of(next, ks1, vs1);
-                page = next, next = page_of(2);
-                for (int j = 0; j < n_tiles; ++j) {
-                    const int s = j % NS;
-                    if (!__all_sync(0xFFFFFFFFu, j < NS || wait(BAR((IS_V ? B_VE : B_KE) + s), ((j / NS) - 1) & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    if (!IS_V && ct < 8) {
-                        // What the softmax needs of the group: the scale of K, the exponent of the
-                        // scale of V and its inverse.  (The slot's last readers are four tiles back.)
-                        const float ev = fmaxf(__log2f(vs), kMinLogScale);
-                        grp_s[(j & 3) * 8 + ct] = make_float4(ks, ev, ex2_approx(-ev), 0.f);
-                    }
-                    uint8_t *dst = sm + (IS_V ? LY::OFF_V : LY::OFF_K) + s * LY::TILE;
-#pragma unroll
-                    for (int k = 0; k < NCH; ++k) {
-                        const int c = ct + NT * k, r = c / CPR, e = c % CPR;
-                        if (c >= BN * CPR) break;
-                        // 128-byte rows of a column half, 16-byte pieces swizzled by the row
-                        uint8_t *row = dst + (e / 4) * BN * 128 + r * 128;
-                        const int a = (e % 4) * 2;
-                        *reinterpret_cast<uint4 *>(row + ((a ^ (r & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_half2(w[k].x & 0xFFFFu), e4m3x2_to_half2(w[k].x >> 16),
-                                       e4m3x2_to_half2(w[k].y & 0xFFFFu), e4m3x2_to_half2(w[k].y >> 16));
-                        *reinterpret_cast<uint4 *>(row + (((a + 1) ^ (r & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_half2(w[k].z & 0xFFFFu), e4m3x2_to_half2(w[k].z >> 16),
-                                       e4m3x2_to_half2(w[k].w & 0xFFFFu), e4m3x2_to_half2(w[k].w >> 16));
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(BAR((IS_V ? B_VF : B_KF) + s));
-                    if (j + 1 < n_tiles) {
-                        // (a V page whose scale is below 2^-90 counts as zeros)
-                        load(j + 1, IS_V && vs1 < kMinScale ? -1 : page);
-                        ks = ks1, vs = vs1;
-                        scales_of(next, ks1, vs1);
-                        page = next, next = page_of(j + 3);
-                    }
-                }
-            };
-            if (n_tiles > 0) {
-                if (warp >= 12) convert(std::false_type{}, std::integral_constant<int, kConvK>{}, tid - 384);
-                else if (warp != 9) convert(std::true_type{}, std::integral_constant<int, kConvV>{}, (warp == 8 ? 0 : warp - 9) * 32 + lane);
-                if (warp == 8 && lane == 0) wait(BAR(B_QF), 0);  // in flight until then
-            }
-        }
+        if (C8 && warp == 8 && lane == 0 && n_tiles > 0) wait(BAR(B_QF), 0);  // in flight until then
         __syncwarp();
     } else {
         reg_alloc<Split<C8>::SOFTMAX>();
@@ -460,52 +475,57 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 const bool masked = !__all_sync(0xFFFFFFFFu, full);
                 // The scores are read 64 columns at a time.  Over bf16 keys all 128 stay
                 // in registers; over the cache, whose converting threads need registers
-                // too, they are read again for the exponentials.
-                constexpr int KEEP = C8 ? 2 : 4;
-                uint32_t r[KEEP][32];
-                auto read = [&](int c0, int n) {
-                    for (int c = 0; c < n; ++c) tmem_ld32(tS + (c0 + c) * 32, r[(c0 + c) % KEEP]);
+                // too, the first 64 are read again for the exponentials.
+                constexpr int KEEP = C8 ? 1 : 2;
+                uint32_t r[KEEP][2][32];
+                auto read = [&](int h) {
+                    uint32_t(&x)[2][32] = r[h % KEEP];
+                    tmem_ld32(tS + h * 64, x[0]);
+                    tmem_ld32(tS + h * 64 + 32, x[1]);
                     tmem_ld_wait();
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < n; ++c) {
-                            const int cb = base + 32 * (c0 + c);
+                        for (int c = 0; c < 2; ++c) {
+                            const int cb = base + h * 64 + c * 32;
                             const uint32_t vm = (low_mask(rr.hi - cb) & ~low_mask(rr.lo - cb)) | low_mask(sink - cb);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                uint32_t &x = r[(c0 + c) % KEEP][e];
-                                x = ((vm >> e) & 1u) ? x : 0xFF800000u;
-                            }
+                            for (int e = 0; e < 32; ++e) x[c][e] = ((vm >> e) & 1u) ? x[c][e] : 0xFF800000u;
                         }
                     }
                 };
-                // row maximum: eight independent ones, over the cache those of the groups
-                constexpr int NG = C8 ? BN / GROUP : 1;  // groups of a tile
-                float pm[8];
+                const float4 *grp = grp_s + (j & 3) * 8;  // of 16 keys each (over the cache)
+                float m_new = m_run;
+                auto maximum = [&](int h) {
+                    const uint32_t(&x)[2][32] = r[h % KEEP];
+                    // four independent ones, over the cache those of the groups
+                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int a = 0; a < 8; ++a) pm[a] = -INFINITY;
-#pragma unroll
-                for (int c0 = 0; c0 < 4; c0 += KEEP) {
-                    read(c0, KEEP);
-#pragma unroll
-                    for (int c = c0; c < c0 + KEEP; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const int a = !C8 ? (e >> 1) & 7 : 2 * c + (GROUP == 16 ? e >> 4 : (e >> 1) & 1);
-                            pm[a] = fmax3(pm[a], __uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1]));
+                            const int a = !C8 ? (e >> 1) & 3 : 2 * c + (GROUP == 16 ? e >> 4 : (e >> 1) & 1);
+                            pm[a] = fmax3(pm[a], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
                         }
-                }
-                const float4 *grp = grp_s + (j & 3) * 8;  // of group a: grp[a * GROUP / 16]
-                if (C8) {
+                    if (!C8) {
+                        m_new = fmaxf(m_new, fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3])) * sl2);
+                    } else {
 #pragma unroll
-                    for (int a = 0; a < NG; ++a) {
-                        const float4 f = grp[a * GROUP / 16];
-                        pm[a] = fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), sl2 * f.x, f.y);
+                        for (int a = 0; a < 64 / (C8 ? GROUP : 64); ++a) {
+                            const float4 f = grp[h * 4 + a * (GROUP / 16)];
+                            m_new = fmaxf(m_new, fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), sl2 * f.x, f.y));
+                        }
                     }
+                };
+                if (C8) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        read(h);
+                        maximum(h);
+                    }
+                } else {
+                    read(0), read(1);
+                    maximum(0), maximum(1);
                 }
-                const float tmax = NG == 4 ? fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3]))
-                                           : fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-                const float m_new = fmaxf(m_run, C8 ? tmax : tmax * sl2);
                 // The rescale touches TMEM with warp-collective loads and stores, so
                 // the whole warp moves when one live row's maximum grew by more than 2^8.
                 if (__any_sync(0xFFFFFFFFu, j == 0 || (live && m_new > m_run + kRescaleLog2))) {
@@ -526,50 +546,57 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     m_run = m_new;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;  // nothing seen yet: every p is 0
-                uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
-                uint64_t ps2[4];
-                float l_tile = 0.f;  // over the cache: the groups' sums, without their scales
+                auto weights = [&](int h) {
+                    const uint32_t(&x)[2][32] = r[h % KEEP];
+                    uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
+                    uint64_t ps2[4];
 #pragma unroll
-                for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (C8) read(half * 2, 2);
+                    for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
                     uint32_t pk[32];
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        const int c = half * 2 + cc;
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             if (C8 && e % (C8 ? GROUP : 32) == 0) {
-                                const float4 f = grp[2 * c + e / 16];
+                                const float4 f = grp[h * 4 + 2 * c + e / 16];
                                 const float k = sl2 * f.x, n = f.y - m_use;
                                 sl2x2 = f2_pack(k, k), negm2 = f2_pack(n, n);
                             }
-                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(r[c % KEEP][e]), __uint_as_float(r[c % KEEP][e + 1])), sl2x2, negm2);
+                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sl2x2, negm2);
                             float p0, p1;
                             f2_unpack(x2, p0, p1);
                             p0 = ex2_approx(p0), p1 = ex2_approx(p1);
                             ps2[(e >> 1) & 3] = f2_add(ps2[(e >> 1) & 3], f2_pack(p0, p1));
-                            pk[cc * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
+                            pk[c * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
                             if (C8 && e % (C8 ? GROUP : 32) == (C8 ? GROUP : 32) - 2) {
+                                // the sum takes P without the scale of V
                                 float a0, a1;
                                 f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
-                                l_tile = fmaf(a0 + a1, grp[2 * c + e / 16].z, l_tile);
+                                l_run = fmaf(a0 + a1, grp[h * 4 + 2 * c + e / 16].z, l_run);
 #pragma unroll
                                 for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
                             }
                         }
+                    tmem_st32(tS + h * 64, pk);
+                    if (!C8) {
+                        float a0, a1;
+                        f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
+                        l_run += a0 + a1;
                     }
-                    tmem_st32(tS + half * 32, pk);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(B_PF + 2 * wg + half));
+                    if (lane == 0) mbar_arrive(BAR(B_PF + 2 * wg + h));
+                };
+                if (C8) {
+#pragma unroll 1
+                    for (int h = FIRST_HALF; h >= 0; --h) {
+                        if (h != FIRST_HALF) read(h);
+                        weights(h);
+                    }
+                } else {
+                    weights(0), weights(1);
                 }
-                float ps[8];
-#pragma unroll
-                for (int a = 0; a < 4; ++a) f2_unpack(ps2[a], ps[2 * a], ps[2 * a + 1]);
-                l_run += C8 ? l_tile : ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
             }
             if (ok && !__all_sync(0xFFFFFFFFu, wait(BAR(B_OF + wg), 0))) ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);

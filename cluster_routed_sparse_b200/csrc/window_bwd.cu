@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     if (!(go = wait_all(B_PF, j & 1))) break;
                     tc_fence_after();
                     mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, j > 0 ? 1u : 0u, 0);
-                    mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, j > 0 ? 1u : 0u, 1);
+                    mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, 1u, 1);
                     commit(leader, BAR(B_1E + s));
                     if (more) {
                         if (!(go = wait_all(B_0F + s2, ph2) && cleaned(B_Z0, j + 1))) break;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     if (!(go = wait_all(B_DF, j & 1))) break;
                     tc_fence_after();
                     mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, j > 0 ? 1u : 0u, 0);
-                    mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, j > 0 ? 1u : 0u, 1);
+                    mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, 1u, 1);
                     commit(leader, BAR(B_0E + s));
                     if (more) {
                         if (!(go = wait_all(B_1F + s2, ph2) && cleaned(B_Z1, j + 1))) break;
