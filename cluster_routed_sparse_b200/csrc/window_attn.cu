@@ -692,7 +692,9 @@ __global__ void __launch_bounds__(128) k_combine(const float *__restrict__ part_
 
 // Parts of the key tiles.  A CTA takes about (tiles + 4) tile times (its start
 // and end cost as much as four), 148 run at once, and joining reads and writes
-// the partial O: one tile time is about 1.1 us.
+// the partial O; a tile time is about 1.9 us, 2.6 us over the cache (a frame of 1,560
+// tokens over 18,720 cached ones: 429, 326, 360, 309 and 314 us with 2, 3, 4, 5 and 7
+// parts).
 struct Plan {
     int TT, tiles_q, nsplit;
 };
@@ -707,7 +709,7 @@ Plan plan(const WinArgs &a) {
     pl.nsplit = 1;
     double best = 1e30;
     for (int s = 1; s <= 64 && s <= std::max<int64_t>(n, 1); ++s) {
-        const double t = (double)((ctas * s + 147) / 148) * ((n + s - 1) / s + 4) * 1.1 + (s > 1 ? 2.5 + rows_us * s : 0.0);
+        const double t = (double)((ctas * s + 147) / 148) * ((n + s - 1) / s + 4) * (a.k8 ? 2.6 : 1.9) + (s > 1 ? 2.5 + rows_us * s : 0.0);
         if (t < best) best = t, pl.nsplit = s;
     }
     return pl;

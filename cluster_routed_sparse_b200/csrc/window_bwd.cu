@@ -58,7 +58,7 @@ enum {
     B_1E = 7,   // [2] L1 stage free
     B_SF = 9,   // S written
     B_DPF = 10, // dP written
-    B_PF = 11,  // P written by the 256 threads
+    B_PF = 11,  // P written by the eight warps
     B_DF = 12,  // dS written
     B_Z0 = 13,  // rows behind the sequence zeroed in the last L0, L1 tile
     B_Z1 = 14,
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         }
         mbar_init(BAR(B_SF), 1);
         mbar_init(BAR(B_DPF), 1);
-        mbar_init(BAR(B_PF), 256);
-        mbar_init(BAR(B_DF), 256);
+        mbar_init(BAR(B_PF), 8);
+        mbar_init(BAR(B_DF), 8);
         mbar_init(BAR(B_Z0), 1);
         mbar_init(BAR(B_Z1), 1);
         mbar_init(BAR(B_AF), 1);
@@ -401,49 +401,47 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             if (!live) full = true;
             const bool masked = !__all_sync(0xFFFFFFFFu, full);
             const float *st = reinterpret_cast<const float *>(sm + LY::OFF_ST + s * kStats * 4) + half * 64;
-            bool got = wait(BAR(B_SF), j & 1);
-            if (KEYS) got = wait(BAR(B_0F + s), (j >> 1) & 1) && got;  // the statistics came with L0
+            bool got = true;
+            float nls[KEYS ? 64 : 1];
+            if (KEYS) {  // the statistics came with L0, before S
+                got = wait(BAR(B_0F + s), (j >> 1) & 1);
+#pragma unroll
+                for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4 *>(nls + (KEYS ? e : 0)) = *reinterpret_cast<const float4 *>(st + e);
+            }
+            got = wait(BAR(B_SF), j & 1) && got;
             if (!__all_sync(0xFFFFFFFFu, got)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            uint32_t x[2][32];
+            uint32_t x[2][32], pk[32];
             tmem_ld32(mS, x[0]);
             tmem_ld32(mS + 32, x[1]);
             tmem_ld_wait();
             // ---- P = 2^(s c - lse)
-            uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 n4 = make_float4(nl, nl, nl, nl);
-                    if (KEYS) n4 = *reinterpret_cast<const float4 *>(st + c * 32 + e);
-                    float y[4];
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), c2, f2_pack(n4.x, n4.y)), y[0], y[1]);
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])), c2, f2_pack(n4.z, n4.w)), y[2], y[3]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) x[c][e + q] = __float_as_uint(ex2_approx(y[q]));
+                for (int e = 0; e < 32; e += 2) {
+                    const float n0 = KEYS ? nls[KEYS ? c * 32 + e : 0] : nl, n1 = KEYS ? nls[KEYS ? c * 32 + e + 1 : 0] : nl;
+                    float y0, y1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), c2, f2_pack(n0, n1)), y0, y1);
+                    x[c][e] = __float_as_uint(ex2_approx(y0)), x[c][e + 1] = __float_as_uint(ex2_approx(y1));
                 }
-            }
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                if (masked) {
                     const uint32_t vm = (low_mask(c_hi - 32 * c) & ~low_mask(c_lo - 32 * c)) | low_mask(c_sink - 32 * c);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[c][e] = ((vm >> e) & 1u) ? x[c][e] : 0u;
                 }
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2)
                     pk[c * 16 + e / 2] = pack_bf16x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+            }
             tmem_st32(mS, pk);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(BAR(B_PF));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_PF));
             // ---- dS = P (dP - delta)
             if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_DPF), j & 1))) {
                 ok = false;
@@ -474,7 +472,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             tmem_st32(mP, pk);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(BAR(B_DF));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_DF));
         }
         if (ok && n_tiles > 0 && !__all_sync(0xFFFFFFFFu, wait(BAR(B_AF), 0))) ok = false;
         tc_fence_after();
