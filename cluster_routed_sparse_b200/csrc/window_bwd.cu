@@ -24,7 +24,7 @@
 // t mod 128, column half t / 128) turn S(j+1) into P while A2(j) and dP(j+1) run,
 // and dP into dS while A1(j+1) and S(j+2) run.  Tensor memory (512 columns):
 // S | dP | A1 | A2, each bf16 operand in the half of its scores that its own
-// threads have read.  P and dS are rounded to bf16 (the operand type), all
+// threads have read; the products of each half start when its four warps are done.  P and dS are rounded to bf16 (the operand type), all
 // else is fp32.  Masks as in window_attn.cu: one column interval per thread.
 #include "stream_device.cuh"
 #include "stream_host.h"
@@ -33,7 +33,7 @@ namespace ac {
 namespace {
 
 constexpr int NTHREADS = 384;
-constexpr uint32_t kRegsMath = 200, kRegsOther = 72;
+constexpr uint32_t kRegsMath = 208, kRegsOther = 88;
 static_assert(2 * 128 * kRegsMath + 128 * kRegsOther <= NTHREADS * 168, "register split exceeds the launch");
 constexpr int kStats = 256;  // floats per query tile: -lse log2(e) of 128 rows, then delta
 
@@ -58,12 +58,12 @@ enum {
     B_1E = 7,   // [2] L1 stage free
     B_SF = 9,   // S written
     B_DPF = 10, // dP written
-    B_PF = 11,  // P written by the eight warps
-    B_DF = 12,  // dS written
-    B_Z0 = 13,  // rows behind the sequence zeroed in the last L0, L1 tile
-    B_Z1 = 14,
-    B_AF = 15,  // accumulators complete
-    NBAR = 16
+    B_PF = 12,  // [2] half of P written by its four warps
+    B_DF = 14,  // [2] half of dS written by its four warps
+    B_Z0 = 16,  // rows behind the sequence zeroed in the last L0, L1 tile
+    B_Z1 = 17,
+    B_AF = 18,  // accumulators complete
+    NBAR = 19
 };
 
 struct BwdMaps {
@@ -216,10 +216,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             mbar_init(BAR(B_1F + i), 1);
             mbar_init(BAR(B_1E + i), 1);
         }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(BAR(B_PF + h), 4);
+            mbar_init(BAR(B_DF + h), 4);
+        }
         mbar_init(BAR(B_SF), 1);
         mbar_init(BAR(B_DPF), 1);
-        mbar_init(BAR(B_PF), 8);
-        mbar_init(BAR(B_DF), 8);
         mbar_init(BAR(B_Z0), 1);
         mbar_init(BAR(B_Z1), 1);
         mbar_init(BAR(B_AF), 1);
@@ -281,21 +283,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     const bool more = j + 1 < n;
                     const int s = j & 1, s2 = s ^ 1, ph2 = ((j + 1) >> 1) & 1;
                     const Desc x1 = KEYS ? m1 : m0;
-                    if (!(go = wait_all(B_PF, j & 1))) break;
-                    tc_fence_after();
-                    mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, j > 0 ? 1u : 0u, 0);
-                    mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, 1u, 1);
-                    commit(leader, BAR(B_1E + s));
-                    if (more) {
-                        if (!(go = wait_all(B_0F + s2, ph2) && cleaned(B_Z0, j + 1))) break;
+                    if (more && !(go = wait_all(B_0F + s2, ph2) && cleaned(B_Z0, j + 1))) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(go = wait_all(B_PF + h, j & 1))) break;
                         tc_fence_after();
+                        mma_weights<64>(leader, tA1, tS, Desc{x1.lo + s * STEP, x1.hi}, ITS, j > 0 || h > 0 ? 1u : 0u, h);
+                    }
+                    if (!go) break;
+                    if (more) {
                         mma_rows<D>(leader, tS, f0, Desc{k0.lo + s2 * STEP, k0.hi}, ISS);
                         commit(leader, BAR(B_SF));
                     }
-                    if (!(go = wait_all(B_DF, j & 1))) break;
-                    tc_fence_after();
-                    mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, j > 0 ? 1u : 0u, 0);
-                    mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, 1u, 1);
+                    commit(leader, BAR(B_1E + s));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(go = wait_all(B_DF + h, j & 1))) break;
+                        tc_fence_after();
+                        mma_weights<64>(leader, tA2, tP, Desc{m0.lo + s * STEP, m0.hi}, ITS, j > 0 || h > 0 ? 1u : 0u, h);
+                    }
+                    if (!go) break;
                     commit(leader, BAR(B_0E + s));
                     if (more) {
                         if (!(go = wait_all(B_1F + s2, ph2) && cleaned(B_Z1, j + 1))) break;
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_PF));
+            if (lane == 0) mbar_arrive(BAR(B_PF + half));
             // ---- dS = P (dP - delta)
             if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_DPF), j & 1))) {
                 ok = false;
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_DF));
+            if (lane == 0) mbar_arrive(BAR(B_DF + half));
         }
         if (ok && n_tiles > 0 && !__all_sync(0xFFFFFFFFu, wait(BAR(B_AF), 0))) ok = false;
         tc_fence_after();

@@ -1,15 +1,15 @@
 // window_few.cu -- the same attention for few query rows: single tokens, or a
 // few, with G * Lq <= 16 rows for each key head, over bf16 keys or the 8-bit cache.
 //
-// Bound by reading K and V once.  A warp takes 16 keys at a time: S = Q K^T with
-// m16n8k16 products (the 16 rows are the packed (token, head) rows of one key
-// head), the running softmax of window_attn.cu, and O += P V.  K and V go from
+// Bound by reading K and V once.  A warp takes 16 keys at a time, and the rows are
+// the short side of m16n8k16 products: S^T = K Q^T, the running softmax of
+// window_attn.cu, O^T += V^T P^T, with P^T transposed in registers.  K and V go from
 // global memory straight into the products' operand registers: the order of the
-// contraction over d, and of the output columns, is free, so each thread owns d / 4
-// consecutive elements of a key row (K) and d / 8 of four value rows (V), loads
-// them 16 bytes at a time, and the rows of a warp are read whole.  The tile
-// kernel would spend its time on the 112 or more empty rows of its products; here
-// the products are a small part of the issue slots.
+// contraction over d, and of the output rows, is free, so each thread owns d / 4
+// consecutive elements of two key rows and d / 8 of four value rows, loads them
+// 16 bytes at a time, and the rows of a warp are read whole.  The tile kernel would
+// spend its time on the 112 or more empty rows of its products; here the products are
+// a small part of the issue slots.
 //
 // The next K rows are loaded as soon as the products of the present ones have
 // taken theirs, and the same for V: every warp has one of the two in flight.
@@ -25,15 +25,21 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kChunk = 16;
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// m16n8k16 with fp32 sums, fp16 or bf16 operands.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// 8 x 8 matrix of 16-bit values, lane (g, t) holding row g, columns 2 t and 2 t + 1, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 struct FewParams {
@@ -60,14 +66,17 @@ __device__ __forceinline__ void load_bytes(uint32_t (&r)[BYTES / 4], const void 
     }
 }
 
-template <int D, bool C8>
-__global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __grid_constant__ FewParams fp) {
+// RT: tiles of 8 rows (1 or 2).  One tile takes few enough registers for another CTA
+// on the SM, hence more loads in flight.
+template <int D, bool C8, int RT>
+__global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(const __grid_constant__ FewParams fp) {
     const WinArgs &p = fp.a;
     constexpr int ES = C8 ? 1 : 2;        // bytes of a stored element
     constexpr int KB = D / 4 * ES;        // bytes of a key row that a thread owns
     constexpr int VB = D / 8 * ES;        // of a value row
     constexpr int KS = D / 16;            // k16 steps of S
-    constexpr int NT = D / 8;             // n8 tiles of O
+    constexpr int DT = D / 16;            // m16 tiles of O^T
+    constexpr int NR = 2 * RT;            // rows of a thread
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
 
     int idx = blockIdx.x;
@@ -88,29 +97,18 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
     const int j0 = (int)((long long)n_all * sp / fp.nsplit), j1 = (int)((long long)n_all * (sp + 1) / fp.nsplit);
     auto chunk_base = [&](int j) { return (j < nsink ? j : w0 + (j - nsink)) * kChunk; };
 
-    // ---- this thread's two rows, g8 and g8 + 8
-    RowRange rr[2];
-    int sink[2];
+    // ---- Q^T as the B operand: k16 step s holds elements t4 D/4 + 4 s + {0..3} of row 8 rt + g8
+    uint32_t bq[RT][KS][2];
+    float g_c[RT];  // scale log2(e), times the power of two taken out of that row
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = g8 + 8 * e, i = r / p.G;
-        rr[e] = RowRange{0, 0x7FFFFFFF};  // a row that does not exist never asks for a mask
-        if (r < rows && i < ql) rr[e] = row_range(p.w, i + off, kl);
-        else if (r < rows) rr[e] = RowRange{0, 0};
-        sink[e] = min(p.w.sinks, rr[e].hi);
-    }
-    // ---- Q as the A operand: k16 step s holds elements t4 D/4 + 4 s + {0..3} of the rows
-    uint32_t aq[KS][4];
-    float row_c[2];  // scale log2(e), times the power of two taken out of the row
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = g8 + 8 * e;
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = g8 + 8 * rt;
         uint32_t w[D / 8];
         const bool live = r < rows && r / p.G < ql;
         const bf16 *src = static_cast<const bf16 *>(p.q.p);
         if (live) src += b * p.q.b + (int64_t)(hk * p.G + r % p.G) * p.q.h + (int64_t)(r / p.G) * p.q.l + t4 * (D / 4);
         load_bytes<D / 2>(w, src, live);
-        row_c[e] = fp.scale_log2;
+        g_c[rt] = fp.scale_log2;
         if constexpr (C8) {
             uint32_t top = 0;
 #pragma unroll
@@ -118,26 +116,37 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             const int ex = min(max((int)(top >> 7) - 127, -120), 120);  // |q| < 2^(ex + 1)
-            row_c[e] *= exp2i(ex);
+            g_c[rt] *= exp2i(ex);
             const float dn = exp2i(-ex);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
-            }
+            for (int i = 0; i < D / 8; ++i) w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
         }
 #pragma unroll
-        for (int s = 0; s < KS; ++s) aq[s][e] = w[2 * s], aq[s][2 + e] = w[2 * s + 1];
+        for (int s = 0; s < KS; ++s) bq[rt][s][0] = w[2 * s], bq[rt][s][1] = w[2 * s + 1];
+    }
+    // ---- this thread's rows of the scores: e = 2 rt + x is row 8 rt + 2 t4 + x
+    RowRange rr[NR];
+    int sink[NR];
+    float row_c[NR];
+#pragma unroll
+    for (int e = 0; e < NR; ++e) {
+        const int r = 8 * (e >> 1) + 2 * t4 + (e & 1), i = r / p.G;
+        rr[e] = RowRange{0, 0x7FFFFFFF};  // a row that does not exist never asks for a mask
+        if (r < rows && i < ql) rr[e] = row_range(p.w, i + off, kl);
+        else if (r < rows) rr[e] = RowRange{0, 0};
+        sink[e] = min(p.w.sinks, rr[e].hi);
+        row_c[e] = __shfl_sync(0xFFFFFFFFu, g_c[e >> 1], 4 * (2 * t4 + (e & 1)));
     }
 
-    // ---- addresses of a chunk's rows
+    // ---- addresses of a chunk's rows.  The table entry is loaded one chunk ahead.
     const int *table = C8 ? p.table + (int64_t)b * p.max_pages : nullptr;
-    float ks = 1.f, vs_next = 1.f;
+    const int log_t = C8 ? 31 - __clz(p.T) : 0;
+    auto entry_of = [&](int j) -> int { return C8 && j < j1 ? __ldg(table + (chunk_base(j) >> log_t)) : 0; };
     struct Rows {
         const uint8_t *k, *v;  // row 0 of the chunk; null: zeros
     };
-    auto rows_of = [&](int base, float &ksc, float &vsc) -> Rows {
+    auto rows_of = [&](int base, int page, float &ksc, float &vsc) -> Rows {
         if constexpr (C8) {
-            const int page = table[base / p.T];
             if (page < 0 || page >= p.pages) {
                 if (lane == 0) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
                 ksc = vsc = 1.f;
@@ -145,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
             }
             const int64_t slot = (int64_t)page * p.Hk + hk;
             ksc = __ldg(p.ks + slot), vsc = __ldg(p.vs + slot);
-            const int64_t at = (slot * p.T + base % p.T) * D;
-            return Rows{p.k8 + at, vsc >= kMinScale ? p.v8 + at : nullptr};
+            const int64_t at = (slot * p.T + (base & (p.T - 1))) * D;
+            return Rows{p.k8 + at, p.v8 + at};
         } else {
             const bf16 *k = static_cast<const bf16 *>(p.k.p) + b * p.k.b + hk * p.k.h + (int64_t)base * p.k.l;
             const bf16 *v = static_cast<const bf16 *>(p.v.p) + b * p.v.b + hk * p.v.h + (int64_t)base * p.v.l;
@@ -168,18 +177,22 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
         }
     };
 
-    float acc[NT][4];
+    float acc[RT][DT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int n = 0; n < DT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[rt][n][e] = 0.f;
+    float m[NR], l[NR];
+#pragma unroll
+    for (int e = 0; e < NR; ++e) m[e] = -INFINITY, l[e] = 0.f;
 
     int j = j0 + warp;
-    float vs = 1.f, ks_next = 1.f;
-    Rows cur{nullptr, nullptr};
+    float ks = 1.f, vs = 1.f, ks_next = 1.f, vs_next = 1.f;
+    int entry = entry_of(j + kWarps);
     if (j < j1) {
-        cur = rows_of(chunk_base(j), ks, vs);
+        const Rows cur = rows_of(chunk_base(j), entry_of(j), ks, vs);
         load_k(cur, chunk_base(j));
         load_v(cur, chunk_base(j));
     }
@@ -188,105 +201,108 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
         const bool more = j + kWarps < j1;
         const int base2 = more ? chunk_base(j + kWarps) : 0;
         Rows nxt{nullptr, nullptr};
-        if (more) nxt = rows_of(base2, ks_next, vs_next);
+        if (more) nxt = rows_of(base2, entry, ks_next, vs_next);
+        entry = entry_of(j + 2 * kWarps);
 
-        float s[2][4];
+        // S^T: s[rt][2 u + x] is key g8 + 8 u, row 8 rt + 2 t4 + x
+        float s[RT][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[rt][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
+        for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
                 if constexpr (C8) {
                     const uint32_t w = kw[u][k];  // 4 codes: one k16 step's share
-                    mma_f16(s[u], aq[k], e4m3x2_to_half2(w & 0xFFFFu), e4m3x2_to_half2(w >> 16));
+                    a[u] = e4m3x2_to_half2(w & 0xFFFFu), a[2 + u] = e4m3x2_to_half2(w >> 16);
                 } else {
-                    mma_bf16(s[u], aq[k], kw[u][2 * k], kw[u][2 * k + 1]);
+                    a[u] = kw[u][2 * k], a[2 + u] = kw[u][2 * k + 1];
                 }
             }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) mma<C8>(s[rt], a[0], a[1], a[2], a[3], bq[rt][k][0], bq[rt][k][1]);
         }
         if (more) load_k(nxt, base2);
 
-        // scores in log2 units; s[u][2 e + c]: row g8 + 8 e, key 8 u + 2 t4 + c
+        // scores in log2 units
         bool full = true;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < NR; ++e) {
             full = full && base + kChunk <= rr[e].hi && (base >= rr[e].lo || base + kChunk <= sink[e]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
             const float c = C8 ? row_c[e] * ks : row_c[e];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) s[u][2 * e + x] *= c;
+            s[e >> 1][e & 1] *= c, s[e >> 1][2 + (e & 1)] *= c;
         }
         if (!full) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < NR; ++e)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int key = base + 8 * u + 2 * t4 + x;
-                        const bool see = key < rr[e].hi && (key >= rr[e].lo || key < sink[e]);
-                        s[u][2 * e + x] = see ? s[u][2 * e + x] : -INFINITY;
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const int key = base + g8 + 8 * u;
+                    float &x = s[e >> 1][2 * u + (e & 1)];
+                    x = key < rr[e].hi && (key >= rr[e].lo || key < sink[e]) ? x : -INFINITY;
+                }
         }
         const float ev = C8 ? fmaxf(__log2f(vs), kMinLogScale) : 0.f;  // exponent of the scale of V
-        float top[2];
+        float top[NR];
+        bool grows = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) top[e] = ev + fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        for (int e = 0; e < NR; ++e) {
+            top[e] = ev + fmaxf(s[e >> 1][e & 1], s[e >> 1][2 + (e & 1)]);
+            grows = grows || top[e] > m[e] + 8.f;
+        }
         // The maximum moves when some row's grew by more than 2^8 (or is the first).
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+        if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < NR; ++e) {
                 float x = top[e];
-                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
                 const float mn = fmaxf(m[e], x);
                 const float al = mn > m[e] ? ex2_approx(m[e] - mn) : 1.f;
                 m[e] = mn;
                 l[e] *= al;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][2 * e] *= al, acc[n][2 * e + 1] *= al;
+                for (int n = 0; n < DT; ++n) acc[e >> 1][n][e & 1] *= al, acc[e >> 1][n][2 + (e & 1)] *= al;
             }
         }
-        uint32_t ap[4];
+        // weights, and P^T as the B operand: keys 8 u + 2 t4 + {0, 1} of row 8 rt + g8
         const float inv_vs = C8 ? ex2_approx(-ev) : 1.f;
+        uint32_t bp[RT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
-            float sum = 0.f;
+        for (int rt = 0; rt < RT; ++rt) {
+            float pr[2][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float p0 = ex2_approx(s[u][2 * e] - mu), p1 = ex2_approx(s[u][2 * e + 1] - mu);
-                sum += p0 + p1;
-                ap[2 * u + e] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
+            for (int x = 0; x < 2; ++x) {
+                const int e = 2 * rt + x;
+                const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
+                pr[0][x] = ex2_approx(s[rt][x] - mu), pr[1][x] = ex2_approx(s[rt][2 + x] - mu);
+                const float sum = pr[0][x] + pr[1][x];
+                l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
             }
-            l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) bp[rt][u] = transpose8x8(C8 ? pack_half2(pr[u][0], pr[u][1]) : pack_bf16x2(pr[u][0], pr[u][1]));
         }
-        // n8 tile n, column g8 is output element g8 D/8 + n
+        // O^T: row g8 of m16 tile n is element g8 D/8 + 2 n, row g8 + 8 the next one.  (Values in a
+        // page with a scale below 2^-90 count as zeros.)
+        if (!C8 || vs >= kMinScale) {
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            uint32_t b0[2], b1[2];
-            if constexpr (C8) {
-                const int word = n / 4, odd = (n / 2) & 1;  // bytes n, n + 1 of the four rows
-                const uint32_t sel = odd ? 0x7362 : 0x5140;
-                const uint32_t x = __byte_perm(vw[0][word], vw[1][word], sel), y = __byte_perm(vw[2][word], vw[3][word], sel);
+            for (int n = 0; n < DT; ++n) {
+                uint32_t a[4];
+                if constexpr (C8) {
+                    const int word = n / 2;  // bytes 2 n, 2 n + 1 of the four rows
+                    const uint32_t sel = n & 1 ? 0x7362 : 0x5140;
+                    const uint32_t x = __byte_perm(vw[0][word], vw[1][word], sel), y = __byte_perm(vw[2][word], vw[3][word], sel);
+                    a[0] = e4m3x2_to_half2(x & 0xFFFFu), a[1] = e4m3x2_to_half2(x >> 16);
+                    a[2] = e4m3x2_to_half2(y & 0xFFFFu), a[3] = e4m3x2_to_half2(y >> 16);
+                } else {
+                    a[0] = __byte_perm(vw[0][n], vw[1][n], 0x5410), a[1] = __byte_perm(vw[0][n], vw[1][n], 0x7632);
+                    a[2] = __byte_perm(vw[2][n], vw[3][n], 0x5410), a[3] = __byte_perm(vw[2][n], vw[3][n], 0x7632);
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    b0[i] = e4m3x2_to_half2((x >> (16 * i)) & 0xFFFFu), b1[i] = e4m3x2_to_half2((y >> (16 * i)) & 0xFFFFu);
-            } else {
-                const uint32_t r0 = vw[0][n / 2], r1 = vw[1][n / 2], r2 = vw[2][n / 2], r3 = vw[3][n / 2];
-                b0[0] = __byte_perm(r0, r1, 0x5410), b0[1] = __byte_perm(r0, r1, 0x7632);
-                b1[0] = __byte_perm(r2, r3, 0x5410), b1[1] = __byte_perm(r2, r3, 0x7632);
-            }
-            if constexpr (C8) {
-                mma_f16(acc[n], ap, b0[0], b1[0]);
-                mma_f16(acc[n + 1], ap, b0[1], b1[1]);
-            } else {
-                mma_bf16(acc[n], ap, b0[0], b1[0]);
-                mma_bf16(acc[n + 1], ap, b0[1], b1[1]);
+                for (int rt = 0; rt < RT; ++rt) mma<C8>(acc[rt][n], a[0], a[1], a[2], a[3], bp[rt][0], bp[rt][1]);
             }
         }
         if (more) load_v(nxt, base2);
@@ -294,21 +310,21 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
     }
 
     // ---- join the four warps
-    __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-    __shared__ __align__(16) float s_o[kWarps][16][D + 4];
+    __shared__ float s_m[kWarps][8 * RT], s_l[kWarps][8 * RT];
+    __shared__ __align__(16) float s_o[kWarps][8 * RT][D + 4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-        if (t4 == 0) s_m[warp][g8 + 8 * e] = m[e], s_l[warp][g8 + 8 * e] = l[e];
-        // columns 2 t4 and 2 t4 + 1 of the n8 tiles: elements (2 t4 + x) D/8 + n
+    for (int e = 0; e < NR; ++e) {
+        const int r = 8 * (e >> 1) + 2 * t4 + (e & 1);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int o = 4; o < 32; o *= 2) l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], o);
+        if (g8 == 0) s_m[warp][r] = m[e], s_l[warp][r] = l[e];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s_o[warp][g8 + 8 * e][(2 * t4 + x) * NT + n] = acc[n][2 * e + x];
+        for (int n = 0; n < DT; ++n)
+            *reinterpret_cast<float2 *>(&s_o[warp][r][g8 * (D / 8) + 2 * n]) =
+                make_float2(acc[e >> 1][n][e & 1], acc[e >> 1][n][2 + (e & 1)]);
     }
     __syncthreads();
-    constexpr int TPR = kThreads / 16;      // threads of a row
+    constexpr int TPR = kThreads / (8 * RT); // threads of a row
     constexpr int EPT = D / TPR;            // elements of a thread
     const int r = tid / TPR, e0 = (tid % TPR) * EPT;
     if (r >= rows) return;
@@ -341,9 +357,8 @@ __global__ void __launch_bounds__(kThreads, C8 ? 3 : 2) k_window_few(const __gri
     } else {
         bf16 *dst = static_cast<bf16 *>(p.o.p) + b * p.o.b + h * p.o.h + (int64_t)i * p.o.l + e0;
 #pragma unroll
-        for (int e = 0; e < EPT; e += 8)
-            *reinterpret_cast<uint4 *>(dst + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                                             pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+        for (int e = 0; e < EPT; e += 4)
+            *reinterpret_cast<uint2 *>(dst + e) = make_uint2(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]));
         if (p.lse && e0 == 0) p.lse[orow] = lse;
     }
 }
@@ -373,12 +388,14 @@ cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s) {
     }
     const int64_t grid = (int64_t)a.B * a.Hk * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    auto go = [&](auto kern) { kern<<<(unsigned)grid, kThreads, 0, s>>>(p); };
+    const bool half = (int64_t)a.G * a.Lq <= 8;
     if (a.d == 128) {
-        if (a.k8) k_window_few<128, true><<<(unsigned)grid, kThreads, 0, s>>>(p);
-        else k_window_few<128, false><<<(unsigned)grid, kThreads, 0, s>>>(p);
+        if (a.k8) half ? go(k_window_few<128, true, 1>) : go(k_window_few<128, true, 2>);
+        else half ? go(k_window_few<128, false, 1>) : go(k_window_few<128, false, 2>);
     } else {
-        if (a.k8) k_window_few<64, true><<<(unsigned)grid, kThreads, 0, s>>>(p);
-        else k_window_few<64, false><<<(unsigned)grid, kThreads, 0, s>>>(p);
+        if (a.k8) half ? go(k_window_few<64, true, 1>) : go(k_window_few<64, true, 2>);
+        else half ? go(k_window_few<64, false, 1>) : go(k_window_few<64, false, 2>);
     }
     AC_NOTE_LAUNCH();
     cudaError_t e = cudaGetLastError();
