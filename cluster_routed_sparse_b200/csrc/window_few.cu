@@ -363,11 +363,20 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
     }
 }
 
-// CTAs for eight waves of single CTAs on the 148 SMs, but no part below 512 keys.
+// Parts of the keys: as many as make the waves of CTAs come out full, a CTA costing
+// its 16-key chunks and about ten more for its start and end, no part below 256 keys.
+// (32,760 cached tokens, 64 key heads in all: 180, 109, 111, 114 and 125 us with 4, 9,
+// 18, 27 and 37 parts.)
 int few_split(const WinArgs &a) {
-    const int64_t n = window_tiles(a.w, a.Lq, a.Lq, a.Lk, kChunk);
-    const int64_t want = (148 * 8 + (int64_t)a.B * a.Hk - 1) / ((int64_t)a.B * a.Hk);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, n / 32));
+    const int64_t n = window_tiles(a.w, a.Lq, a.Lq, a.Lk, kChunk), units = (int64_t)a.B * a.Hk;
+    const int64_t slots = 148 * ((a.k8 ? 5 : 4) - ((int64_t)a.G * a.Lq <= 8 ? 1 : 2));
+    int64_t best = INT64_MAX;
+    int parts = 1;
+    for (int s = 1; s <= 256 && s <= std::max<int64_t>(n / 16, 1); ++s) {
+        const int64_t t = ((units * s + slots - 1) / slots) * ((n + s - 1) / s + 10);
+        if (t < best) best = t, parts = s;
+    }
+    return parts;
 }
 
 }  // namespace
