@@ -17,15 +17,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMinExp = -120, kMaxExp = 119;  // 448 * 2^119 is the largest that fp32 and bf16 hold
 
-// NC chunks of 8 elements per thread: NC * kThreads * 8 >= T * d.
-template <int NC>
-__global__ void __launch_bounds__(kThreads) k_cache8_append(const AppendArgs a, int touched) {
-    int64_t idx = blockIdx.x;
-    const int blk_i = (int)(idx % touched);
-    idx /= touched;
+// NC chunks of 8 elements per thread: NC * kThreads * 8 >= T * D.
+template <int D, int NC>
+__global__ void __launch_bounds__(kThreads, NC > 4 ? 3 : 6) k_cache8_append(const AppendArgs a, int touched) {
+    uint32_t idx = blockIdx.x;  // (page of the sequence, K or V, head, sequence)
+    const int blk_i = idx % (uint32_t)touched;
+    idx /= (uint32_t)touched;
     const bool is_v = idx & 1;
     idx >>= 1;
-    const int h = (int)(idx % a.Hk), b = (int)(idx / a.Hk);
+    const int h = idx % (uint32_t)a.Hk, b = idx / (uint32_t)a.Hk;
     const int start = a.start[b];
     int n = a.n;
     if (a.counts) n = min(max(a.counts[b], 0), a.n);
@@ -33,38 +33,48 @@ __global__ void __launch_bounds__(kThreads) k_cache8_append(const AppendArgs a, 
         if (threadIdx.x == 0) atomicOr(&a.err->bits, DEV_ERR_BOUNDS);
         return;
     }
-    const int64_t blk = start / a.T + blk_i;
-    const int64_t first = blk * a.T - start;  // token index of the page's slot 0
-    if (first >= n || n == 0) return;
+    const int log_t = 31 - __clz(a.T);
+    const int64_t blk = (start >> log_t) + blk_i;
+    const int64_t first64 = blk * a.T - start;  // token index of the page's slot 0
+    if (first64 >= n || n == 0) return;
+    const int first = (int)first64;
     const int page = blk < a.max_pages ? a.table[(int64_t)b * a.max_pages + blk] : -1;
     if (page < 0 || page >= a.pages) {
         if (threadIdx.x == 0) atomicOr(&a.err->bits, DEV_ERR_BOUNDS);
         return;
     }
-    const int cpr = a.d / 8, chunks = a.T * cpr;
+    constexpr int CPR = D / 8;  // chunks of a row
+    const int chunks = a.T * CPR;
     const View &src = is_v ? a.v : a.k;
     const bf16 *x = static_cast<const bf16 *>(src.p) + b * src.b + h * src.h;
     const int64_t slot = (int64_t)page * a.Hk + h;
-    uint8_t *codes = (is_v ? a.v8 : a.k8) + slot * a.T * a.d;
+    uint8_t *codes = (is_v ? a.v8 : a.k8) + slot * a.T * D;
     float *scale = (is_v ? a.vs : a.ks) + slot;
 
     uint4 w[NC];
-    uint32_t top = 0;  // largest |value| as bf16 bits: ordered like the values
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int ch = c * kThreads + threadIdx.x;
-        const int64_t tok = first + ch / cpr;
+        const int ch = c * kThreads + threadIdx.x, tok = first + ch / CPR;
         w[c] = make_uint4(0, 0, 0, 0);
-        if (ch < chunks && tok >= 0 && tok < n) w[c] = *reinterpret_cast<const uint4 *>(x + tok * src.l + (ch % cpr) * 8);
+        if (ch < chunks && tok >= 0 && tok < n) w[c] = *reinterpret_cast<const uint4 *>(x + tok * src.l + (ch % CPR) * 8);
     }
+    // largest |value|: bf16 bits without the sign are ordered like the values
+    uint32_t top2 = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = u[i] & 0x7FFFu, hi = (u[i] >> 16) & 0x7FFFu;
-            top = max(top, lo > 0x7F80u ? 0u : lo);  // NaN has no size
-            top = max(top, hi > 0x7F80u ? 0u : hi);
+        for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, u[i] & 0x7FFF7FFFu);
+    }
+    uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    if (top > 0x7F80u) {  // a NaN, which has no size: once more without it
+        top = 0;
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = u[i] & 0x7FFFu, hi = (u[i] >> 16) & 0x7FFFu;
+                top = max(top, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
+            }
         }
     }
     __shared__ uint32_t s_top;
@@ -89,17 +99,19 @@ __global__ void __launch_bounds__(kThreads) k_cache8_append(const AppendArgs a, 
     const float down = shift < -126 ? 0.f : exp2i(min(shift, 0));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int ch = c * kThreads + threadIdx.x;
-        const int64_t tok = first + ch / cpr;
+        const int ch = c * kThreads + threadIdx.x, tok = first + ch / CPR;
         if (ch >= chunks) continue;
-        uint2 *dst = reinterpret_cast<uint2 *>(codes + (int64_t)ch * 8);
+        uint2 *dst = reinterpret_cast<uint2 *>(codes + ch * 8);
         if (tok >= 0 && tok < n) {
             const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
             uint32_t q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                q[i] = floats_to_e4m3x2(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
-            *dst = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+            for (int i = 0; i < 4; ++i) {
+                float x0, x1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)), f2_pack(up, up)), x0, x1);
+                q[i] = floats_to_e4m3x2(x0, x1);
+            }
+            *dst = make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
         } else if (tok < 0 && shift < 0) {
             const uint2 old = *dst;
             const uint32_t u[2] = {old.x, old.y};
@@ -121,15 +133,12 @@ cudaError_t launch_cache8_append(const AppendArgs &a, cudaStream_t s) {
     const int touched = (a.n + a.T - 1) / a.T + 1;
     const int64_t grid = (int64_t)a.B * a.Hk * 2 * touched;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    auto go = [&](auto kern) { kern<<<(unsigned)grid, kThreads, 0, s>>>(a, touched); };
     const int nc = (a.T * a.d / 8 + kThreads - 1) / kThreads;
-    if (nc <= 1)
-        k_cache8_append<1><<<(unsigned)grid, kThreads, 0, s>>>(a, touched);
-    else if (nc <= 2)
-        k_cache8_append<2><<<(unsigned)grid, kThreads, 0, s>>>(a, touched);
-    else if (nc <= 4)
-        k_cache8_append<4><<<(unsigned)grid, kThreads, 0, s>>>(a, touched);
+    if (a.d == 128)
+        nc <= 1 ? go(k_cache8_append<128, 1>) : nc <= 2 ? go(k_cache8_append<128, 2>) : nc <= 4 ? go(k_cache8_append<128, 4>) : go(k_cache8_append<128, 8>);
     else
-        k_cache8_append<8><<<(unsigned)grid, kThreads, 0, s>>>(a, touched);
+        nc <= 1 ? go(k_cache8_append<64, 1>) : nc <= 2 ? go(k_cache8_append<64, 2>) : go(k_cache8_append<64, 4>);
     AC_NOTE_LAUNCH();
     return cudaGetLastError();
 }
