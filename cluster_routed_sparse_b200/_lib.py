@@ -130,7 +130,7 @@ SIGNATURES = {
                           ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I), _I, _I, _I, _P]),
     "ac_window_attn_workspace": (_I, [_I] * 6 + [_WN, _I64P]),
     "ac_window_attn": (_I, [_VW] * 4 + [_P] + [_I] * 6 + [_P, _P, _WN, _P, ctypes.c_int64, _P]),
-    "ac_window_attn_backward_workspace": (_I, [_I] * 6 + [_I64P]),
+    "ac_window_attn_backward_workspace": (_I, [_I] * 6 + [_WN, _I64P]),
     "ac_window_attn_backward": (_I, [_VW] * 5 + [_P] + [_VW] * 3 + [_I] * 6 + [_P, _P, _WN, _P, ctypes.c_int64, _P]),
     "ac_cache8_append": (_I, [_C8, _VW, _VW, _I, _I, _P, _I, _P, _P, _P]),
     "ac_cache8_attn_workspace": (_I, [_C8, _I, _I, _I, _I, _WN, _I64P]),

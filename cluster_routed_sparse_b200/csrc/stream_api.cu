@@ -193,11 +193,12 @@ extern "C" ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac
 }
 
 extern "C" ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
-                                                       int32_t d, int64_t *bytes) {
+                                                       int32_t d, const ac_window *w, int64_t *bytes) {
     if (!bytes) return refuse("ac_window_attn_backward_workspace: NULL argument");
-    const ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
-    if (st != AC_OK) return st;
+    ac_status st = check_sizes(B, Hq, Hk, Lq, Lk, d);
     WinArgs a{};
+    if (st == AC_OK) st = window_rule(w, d, &a.w, &a.scale);
+    if (st != AC_OK) return st;
     a.B = B, a.Hq = Hq, a.Hk = Hk, a.G = Hq / Hk, a.Lq = Lq, a.Lk = Lk, a.d = d;
     *bytes = window_bwd_workspace(a);
     return AC_OK;
@@ -214,7 +215,7 @@ extern "C" ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *
     WinArgs &a = g.f;
     if (st == AC_OK) st = window_rule(w, d, &a.w, &a.scale);
     int64_t need = 0;
-    if (st == AC_OK) st = ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, &need);
+    if (st == AC_OK) st = ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, w, &need);
     if (st != AC_OK) return st;
     if (B == 0 || (Lq == 0 && Lk == 0)) return AC_OK;
     if ((Lq > 0 && (!lse || !rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq) || !rows16(d_o, B, Hq, Lq) ||

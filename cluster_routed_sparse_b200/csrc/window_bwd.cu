@@ -20,6 +20,10 @@
 // part of those roundings which is common to all keys leaves too.  The second
 // role takes the corrected delta0 + r.
 //
+// A key tile that many queries see (first tokens; early keys without a left bound)
+// would keep one SM busy after the others are done: its query tiles are split into
+// parts of at most `chunk`, whose fp32 dK and dV k_sum_parts adds, in order.
+//
 // Schedule: A1(j), S(j+1), A2(j), dP(j+1) on the tensor core; 256 threads (row
 // t mod 128, column half t / 128) turn S(j+1) into P while A2(j) and dP(j+1) run,
 // and dP into dS while A1(j+1) and S(j+2) run.  Tensor memory (512 columns):
@@ -73,6 +77,8 @@ struct BwdMaps {
 struct BwdParams {
     View dq, dk, dv;
     float *stats;  // [B Hk][tiles_q][kStats]
+    float *parts;  // [B Hk][part_tiles][max_parts][2][128][d]: dV, dK of key tiles in parts
+    int chunk, max_parts, part_tiles;  // query tiles of a part; key tiles of a head that may have parts
     const int *q_lens, *k_lens;
     int B, Hq, Hk, G, TT, Lq, Lk, tiles_q, tiles_k;
     WinRule w;
@@ -98,6 +104,22 @@ __device__ __forceinline__ RowRange key_range(const WinRule &w, int j, int off, 
     lo = lo < 0 ? 0 : lo > ql ? ql : lo;
     hi = hi < lo ? lo : hi > ql ? ql : hi;
     return RowRange{(int)lo, (int)hi};
+}
+
+// Query tiles [lo, lo + n) that see the key tile at key r0, and the parts they come in.
+struct KeyTile {
+    int lo, n, parts;
+};
+__device__ __forceinline__ KeyTile key_tile(const BwdParams &p, int r0, int ql, int kl) {
+    KeyTile t{0, 0, 1};
+    if (r0 < kl) {
+        const RowRange a = key_range(p.w, r0, kl - ql, ql, kl);
+        const RowRange z = key_range(p.w, min(r0 + 127, kl - 1), kl - ql, ql, kl);
+        const int hi = max(a.hi, z.hi);
+        if (hi > a.lo) t.lo = a.lo / p.TT, t.n = (hi + p.TT - 1) / p.TT - t.lo;
+    }
+    if (r0 / 128 < p.part_tiles) t.parts = max(1, min((t.n + p.chunk - 1) / p.chunk, p.max_parts));
+    return t;
 }
 
 // -lse log2(e) (-inf for a row without keys, so that its P is 0) and
@@ -155,8 +177,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     // ---- work item: (sequence and key head, row tile).  The row tiles with the most
     // columns first: early keys (first tokens; no left bound), late queries.
     const int tiles = KEYS ? p.tiles_k : p.tiles_q;
-    const int bh = blockIdx.x / tiles;
-    const int rt = KEYS ? blockIdx.x % tiles : tiles - 1 - blockIdx.x % tiles;
+    const int part = KEYS ? blockIdx.x % p.max_parts : 0, item = KEYS ? blockIdx.x / p.max_parts : blockIdx.x;
+    const int bh = item / tiles;
+    const int rt = KEYS ? item % tiles : tiles - 1 - item % tiles;
     const int b = bh / p.Hk, hk = bh % p.Hk;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
     const int off = kl - ql;
@@ -165,15 +188,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     int lo_c = 0, n_tiles = 0, nsink = 0;  // lo_c: first tile (behind the first tokens' tiles)
     bool tail = false;                     // the last tile holds rows behind the sequence that TMA does not zero
     int tail_row = 0;
+    int parts = 1;
     if (KEYS) {
-        if (r0 < kl) {
-            const RowRange a = key_range(p.w, r0, off, ql, kl);
-            const RowRange z = key_range(p.w, min(r0 + 127, kl - 1), off, ql, kl);
-            const int hi = max(a.hi, z.hi);
-            if (hi > a.lo) lo_c = a.lo / p.TT, n_tiles = (hi + p.TT - 1) / p.TT - lo_c;
-            tail = n_tiles > 0 && (lo_c + n_tiles) * p.TT > ql && ql < p.Lq;
-            tail_row = (ql - (lo_c + n_tiles - 1) * p.TT) * p.G;
-        }
+        const KeyTile t = key_tile(p, r0, ql, kl);
+        parts = t.parts;
+        if (part >= parts) return;  // (the whole CTA, before it holds anything)
+        const int j0 = (int)((long long)t.n * part / parts), j1 = (int)((long long)t.n * (part + 1) / parts);
+        lo_c = t.lo + j0, n_tiles = j1 - j0;
+        tail = n_tiles > 0 && (lo_c + n_tiles) * p.TT > ql && ql < p.Lq;
+        tail_row = (ql - (lo_c + n_tiles - 1) * p.TT) * p.G;
     } else if (r0 < ql) {
         const int lo = row_range(p.w, r0 + off, kl).lo;
         const int hi = row_range(p.w, min(r0 + p.TT, ql) - 1 + off, kl).hi;
@@ -497,6 +520,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             const float f = half ? p.scale : 1.f;
             const bool store = ok && r0 + row < p.Lk;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(v.p) + b * v.b + hk * v.h + (int64_t)(r0 + row) * v.l);
+            float4 *dst4 = nullptr;
+            if (parts > 1)
+                dst4 = reinterpret_cast<float4 *>(
+                    p.parts + (((((int64_t)bh * p.part_tiles + rt) * p.max_parts + part) * 2 + half) * 128 + row) * D);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -504,7 +531,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     tmem_ld32(tmem + lane_off + (half ? tA2 : tA1) + c * 32, o);
                     tmem_ld_wait();
                 }
-                if (store) {
+                if (store && parts > 1) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float *x = reinterpret_cast<const float *>(o + 4 * q);
+                        dst4[c * 8 + q] = some ? make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                } else if (store) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float *x = reinterpret_cast<const float *>(o + 8 * q);
@@ -513,6 +546,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                                               : make_uint4(0, 0, 0, 0);
                     }
                 }
+                __syncwarp();
             }
         } else {
             // dQ = scale (A2 - r A1), half the columns each
@@ -551,6 +585,30 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     }
 }
 
+// dV and dK of the key tiles in parts: the parts' sums in order.  One thread for four
+// elements of a row.
+template <int D>
+__global__ void __launch_bounds__(256) k_sum_parts(const BwdParams p) {
+    const int tile = blockIdx.x % p.part_tiles, bh = blockIdx.x / p.part_tiles;
+    const int b = bh / p.Hk, hk = bh % p.Hk, r0 = tile * 128;
+    const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
+    const int parts = key_tile(p, r0, ql, kl).parts;
+    if (parts == 1) return;
+    const float4 *src = reinterpret_cast<const float4 *>(p.parts + ((int64_t)bh * p.part_tiles + tile) * p.max_parts * 2 * 128 * D);
+    for (int t = blockIdx.y * 256 + threadIdx.x; t < 2 * 128 * D / 4; t += gridDim.y * 256) {
+        const int half = t / (128 * D / 4), row = t / (D / 4) % 128, e = t % (D / 4) * 4;
+        if (r0 + row >= p.Lk) continue;
+        float4 s = src[t];
+        for (int i = 1; i < parts; ++i) {
+            const float4 x = src[(int64_t)i * (2 * 128 * D / 4) + t];
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+        const View &v = half ? p.dk : p.dv;
+        *reinterpret_cast<uint2 *>(static_cast<bf16 *>(v.p) + b * v.b + hk * v.h + (int64_t)(r0 + row) * v.l + e) =
+            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+}
+
 int64_t query_tiles(const WinArgs &a) {
     const int TT = 128 / a.G;
     return (a.Lq + TT - 1) / TT;
@@ -558,7 +616,39 @@ int64_t query_tiles(const WinArgs &a) {
 
 }  // namespace
 
-int64_t window_bwd_workspace(const WinArgs &a) { return (int64_t)a.B * a.Hk * query_tiles(a) * kStats * 4; }
+namespace {
+
+// Parts of the key tiles' work.  A part takes at most half of what an SM has to do on
+// average, and eight query tiles at least.
+struct Parts {
+    int chunk, max_parts, part_tiles;
+};
+
+Parts plan_parts(const WinArgs &a) {
+    const int64_t all = query_tiles(a), tiles_k = (a.Lk + 127) / 128, heads = (int64_t)a.B * a.Hk;
+    Parts pt{1 << 30, 1, 0};
+    if (all == 0 || tiles_k == 0) return pt;
+    const int64_t window = std::min(all, window_tiles(a.w, 128, a.Lk, a.Lq, 128 / a.G));  // of keys without the first tokens
+    const int64_t first = a.w.left < 0 ? tiles_k : std::min<int64_t>(tiles_k, (a.w.sinks + (int64_t)127) / 128);
+    const int64_t total = a.w.left < 0 ? heads * tiles_k * (a.w.right < 0 ? all : (all + 1) / 2)
+                                       : heads * (first * all + (tiles_k - first) * window);
+    const int64_t chunk = std::max<int64_t>(8, (total + 2 * 148 - 1) / (2 * 148));
+    const int64_t most = first > 0 ? all : window;
+    if (most <= chunk) return pt;
+    pt.chunk = (int)chunk;
+    pt.max_parts = (int)std::min<int64_t>((most + chunk - 1) / chunk, 64);
+    pt.part_tiles = (int)(window > chunk ? tiles_k : first);
+    return pt;
+}
+
+int64_t stats_floats(const WinArgs &a) { return (int64_t)a.B * a.Hk * query_tiles(a) * kStats; }
+
+}  // namespace
+
+int64_t window_bwd_workspace(const WinArgs &a) {
+    const Parts pt = plan_parts(a);
+    return (stats_floats(a) + (int64_t)a.B * a.Hk * pt.part_tiles * pt.max_parts * 2 * 128 * a.d) * 4;
+}
 
 cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     const WinArgs &a = g.f;
@@ -570,7 +660,10 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     p.tiles_q = (int)query_tiles(a), p.tiles_k = (a.Lk + 127) / 128;
     p.w = a.w, p.scale = a.scale, p.scale_log2 = a.scale * 1.44269504088896f;
     p.launch = next_launch_id(), p.err = a.err;
-    const int64_t nq = (int64_t)a.B * a.Hk * p.tiles_q, nk = (int64_t)a.B * a.Hk * p.tiles_k;
+    const Parts pt = plan_parts(a);
+    p.parts = p.stats + stats_floats(a);
+    p.chunk = pt.chunk, p.max_parts = pt.max_parts, p.part_tiles = pt.part_tiles;
+    const int64_t nq = (int64_t)a.B * a.Hk * p.tiles_q, nk = (int64_t)a.B * a.Hk * p.tiles_k * pt.max_parts;
     const int64_t stat_blocks = nq * 128 * (a.d / 8) / 256;
     if (nq > 0x7FFFFFFF || nk > 0x7FFFFFFF || stat_blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     BwdMaps mq{}, mk{};  // rows = queries; rows = keys
@@ -606,6 +699,13 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     } else {
         go(k_window_bwd<64, false>, Layout<64>::SMEM, mq, nq);
         go(k_window_bwd<64, true>, Layout<64>::SMEM, mk, nk);
+    }
+    if (e == cudaSuccess && pt.part_tiles > 0) {
+        const dim3 grid((unsigned)((int64_t)a.B * a.Hk * pt.part_tiles), 8);
+        if (a.d == 128) k_sum_parts<128><<<grid, 256, 0, s>>>(p);
+        else k_sum_parts<64><<<grid, 256, 0, s>>>(p);
+        AC_NOTE_LAUNCH();
+        e = cudaGetLastError();
     }
     return e;
 }

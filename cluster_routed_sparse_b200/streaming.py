@@ -190,7 +190,8 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
 @functools.lru_cache(maxsize=1024)
 def _backward_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block):
     n = ctypes.c_int64(0)
-    check(_lib.load().ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, ctypes.byref(n)))
+    check(_lib.load().ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, _window(left, right, sinks, block, 0.0),
+                                                        ctypes.byref(n)))
     return n.value
 
 

@@ -482,7 +482,7 @@ AC_API ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac_vie
  * heads get the sum.  Rows behind a sequence get zeros.  Bit-identical from run
  * to run (no atomic sums).  Errors as ac_window_attn. */
 AC_API ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
-                                                   int32_t d, int64_t *bytes);
+                                                   int32_t d, const ac_window *w, int64_t *bytes);
 AC_API ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *q, const ac_view *k, const ac_view *v,
                                          const ac_view *o, const float *lse, const ac_view *dq, const ac_view *dk,
                                          const ac_view *dv, int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,

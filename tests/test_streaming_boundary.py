@@ -73,11 +73,11 @@ def test_workspaces_are_checked():
     if n.value:
         assert attn(Lq=1, Lk=1 << 20, w=window(-1), nbytes=n.value - 1) == WORKSPACE
         assert attn(Lq=1, Lk=1 << 20, w=window(-1), ws=None, nbytes=n.value) == WORKSPACE
-    assert lib.ac_window_attn_backward_workspace(1, 4, 2, 8, 8, 64, ctypes.byref(n)) == 0
+    assert lib.ac_window_attn_backward_workspace(1, 4, 2, 8, 8, 64, window(), ctypes.byref(n)) == 0
     if n.value:
         assert backward(nbytes=n.value - 1) == WORKSPACE
     assert lib.ac_window_attn_workspace(1, 4, 2, 8, 8, 64, window(), None) == INVALID
-    assert lib.ac_window_attn_backward_workspace(1, 4, 2, 8, 8, 64, None) == INVALID
+    assert lib.ac_window_attn_backward_workspace(1, 4, 2, 8, 8, 64, window(), None) == INVALID
     assert backward(lse=None) == INVALID
 
 
