@@ -372,9 +372,10 @@ int few_split(const WinArgs &a) {
     const int64_t slots = 148 * ((a.k8 ? 5 : 4) - ((int64_t)a.G * a.Lq <= 8 ? 1 : 2));
     int64_t best = INT64_MAX;
     int parts = 1;
-    for (int s = 1; s <= 256 && s <= std::max<int64_t>(n / 16, 1); ++s) {
+    for (int64_t waves = 0; waves <= 8; ++waves) {
+        const int64_t s = std::min(std::max<int64_t>(waves * slots / units, 1), std::max<int64_t>(n / 16, 1));
         const int64_t t = ((units * s + slots - 1) / slots) * ((n + s - 1) / s + 10);
-        if (t < best) best = t, parts = s;
+        if (t < best) best = t, parts = (int)s;
     }
     return parts;
 }

@@ -13,6 +13,10 @@ Each call forwards data pointers, strides and the current stream of the
 tensors' device to the C ABI in include/ac.h, which documents the operators;
 all arithmetic runs in libac's kernels.  Tensors are [B, H, L, d] in any strides
 (d contiguous).  Nothing here synchronises but ops_status.
+
+The common case of a call (new outputs, tensors on the current device) goes
+through the compiled _fast module, which makes the same C calls; what it does
+not take comes back as None and is checked, explained or done here.
 """
 from __future__ import annotations
 
@@ -25,8 +29,20 @@ import torch
 from . import _lib
 from ._lib import ACCache8, ACView, ACWindow, check
 
+try:
+    from . import _fast
+except ImportError:  # built with libac.so; without it every call takes the way below
+    _fast = None
+
 _ROPE_DTYPES = {torch.bfloat16: _lib.AC_DTYPE_BF16, torch.float16: _lib.AC_DTYPE_F16, torch.float32: _lib.AC_DTYPE_F32}
 _NO_VIEW = ACView(None, 0, 0, 0)
+
+
+def _took(result):
+    """Whether _fast made the call; raises what the library refused."""
+    if result.__class__ is int:
+        check(result)
+    return result is not None
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -75,6 +91,11 @@ def _ints(t, name, device, shape):
 
 
 # ---------------------------------------------------------------- rotary embedding
+def _arrays(freq, pairs):
+    f, n = (ctypes.c_double * max(1, len(freq)))(*freq), (ctypes.c_int32 * max(1, len(pairs)))(*pairs)
+    return f, n, ctypes.addressof(f), ctypes.addressof(n)
+
+
 @functools.lru_cache(maxsize=64)
 def _axes(pairs, theta):
     """Frequencies of the pairs: axis i has the series theta^(-k / pairs[i]) of its own."""
@@ -82,14 +103,14 @@ def _axes(pairs, theta):
     if len(theta) != len(pairs) or any(n < 0 for n in pairs) or any(not t > 0 for t in theta):
         raise ValueError("one theta > 0 for all axes, or one for each; pairs >= 0")
     freq = [t ** (-k / n) for n, t in zip(pairs, theta) for k in range(n)]
-    return (ctypes.c_double * max(1, len(freq)))(*freq), (ctypes.c_int32 * max(1, len(pairs)))(*pairs)
+    return _arrays(freq, pairs)
 
 
 @functools.lru_cache(maxsize=64)
 def _axes_given(pairs, freqs):
     if len(freqs) != sum(pairs):
         raise ValueError("one frequency for each pair")
-    return (ctypes.c_double * max(1, len(freqs)))(*freqs), (ctypes.c_int32 * max(1, len(pairs)))(*pairs)
+    return _arrays(freqs, pairs)
 
 
 def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved: bool = True, inverse: bool = False,
@@ -105,6 +126,16 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
     the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
     fp32.  Returns (q, k) rotated, or q alone when k is None."""
+    pairs = tuple(pairs)
+    axes = len(pairs)
+    if freqs is not None:
+        freq, npairs, pf, pn = _axes_given(pairs, tuple(freqs))
+    else:
+        freq, npairs, pf, pn = _axes(pairs, tuple(theta) if isinstance(theta, (list, tuple)) else theta)
+    if _fast is not None and out is None:
+        r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), 1 if interleaved else 0, 1 if inverse else 0)
+        if _took(r):
+            return r
     dt = q.dtype
     dtype = _ROPE_DTYPES.get(dt)
     if dtype is None:
@@ -113,12 +144,6 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     shape = _shape(q, "q")
     vq = _view(q, "q", dev, shape, dt)
     B, Hq, L, d = shape
-    pairs = tuple(pairs)
-    axes = len(pairs)
-    if freqs is not None:
-        freq, npairs = _axes_given(pairs, tuple(freqs))
-    else:
-        freq, npairs = _axes(pairs, tuple(theta) if isinstance(theta, (list, tuple)) else theta)
     if positions.dim() == 3:
         pos, pos_b = _ints(positions, "positions", dev, (B, L, axes)), L * axes
     else:
@@ -170,6 +195,10 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
     `block` tokens, plus the first `sinks` tokens (ac_window_attn; struct
     ac_window says exactly which keys a query sees).  q_lens, k_lens: int32 [B]
     lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32."""
+    if _fast is not None and out is None:
+        r = _fast.window(q, k, v, left, right, sinks, block, float(scale), q_lens, k_lens, bool(return_lse))
+        if _took(r):
+            return r
     dev = q.device
     shape = _shape(q, "q")
     B, Hq, Lq, d = shape
@@ -257,6 +286,8 @@ def cache8_append(k, v, cache: Cache8, page_table, start, counts=None):
     """Write the new tokens k, v [B, heads, n, d] (bf16) of each sequence behind its
     first start[b] tokens into the cache (ac_cache8_append).  page_table: int32
     [B, max_pages]; start, counts: int32 [B] (counts: how many of the n are real)."""
+    if _fast is not None and _took(_fast.append(k, v, *cache, page_table, start, counts)):
+        return
     dev = k.device
     shape = _shape(k, "k")
     B, H, n, d = shape
@@ -285,6 +316,10 @@ def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: 
                 q_lens=None, scale: float = 0.0, out=None, return_lse: bool = False):
     """window_attn of q [B, Hq, Lq, d] over the first k_lens[b] cached tokens of each
     sequence (ac_cache8_attn)."""
+    if _fast is not None and out is None:
+        r = _fast.cache_attn(q, *cache, page_table, k_lens, left, right, sinks, block, float(scale), q_lens, bool(return_lse))
+        if _took(r):
+            return r
     dev = q.device
     shape = _shape(q, "q")
     vq = _view(q, "q", dev, shape)
