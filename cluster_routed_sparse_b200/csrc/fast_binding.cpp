@@ -169,6 +169,51 @@ PyObject *window(PyObject *, PyObject *const *args, Py_ssize_t n) {
     CATCH
 }
 
+// backward(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens)
+PyObject *backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    try {
+        Window win;
+        if (n != 13 || !win.read(args + 6)) return none();
+        const Tensor *t[6];
+        for (int i = 0; i < 6; ++i)
+            if (!(t[i] = tensor(args[i])) || !t[i]->is_cuda()) return none();
+        const c10::DeviceIndex dev = t[1]->get_device();
+        ac_view v[5];
+        if (dev != c10::cuda::current_device()) return none();
+        for (int i = 0; i < 5; ++i)
+            if (!rows(*t[i], at::kBFloat16, dev, &v[i])) return none();
+        const int64_t B = t[1]->size(0), Hq = t[1]->size(1), Lq = t[1]->size(2), d = t[1]->size(3);
+        const int64_t Hk = t[2]->size(1), Lk = t[2]->size(2);
+        const Tensor &lse = *t[5];
+        const int32_t *ql, *kl;
+        if (!same(*t[0], B, Hq, Lq, d) || !same(*t[4], B, Hq, Lq, d) || !same(*t[2], B, Hk, Lk, d) || !same(*t[3], B, Hk, Lk, d) ||
+            !on(lse, at::kFloat, dev) || lse.dim() != 3 || lse.size(0) != B || lse.size(1) != Hq || lse.size(2) != Lq ||
+            !lse.is_contiguous() || !lens(args[11], B, dev, &ql) || !lens(args[12], B, dev, &kl) || !fits(B) || !fits(Hq) ||
+            !fits(Hk) || !fits(Lq) || !fits(Lk) || !fits(d))
+            return none();
+        int64_t bytes = 0;
+        ac_status st = ac_window_attn_backward_workspace((int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d,
+                                                         &win.w, &bytes);
+        if (st != AC_OK) return error(st);
+        const Tensor dq = like(*t[1], {B, Hq, Lq, d}, at::kBFloat16), dk = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16),
+                     dv = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16);
+        const Tensor ws = bytes ? like(*t[1], {bytes}, at::kByte) : Tensor();
+        const ac_view vdq{dq.data_ptr(), Hq * Lq * d, Lq * d, d}, vdk{dk.data_ptr(), Hk * Lk * d, Lk * d, d},
+            vdv{dv.data_ptr(), Hk * Lk * d, Lk * d, d};
+        st = ac_window_attn_backward(&v[0], &v[1], &v[2], &v[3], &v[4], static_cast<const float *>(lse.data_ptr()), &vdq, &vdk, &vdv,
+                                     (int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, ql, kl, &win.w,
+                                     bytes ? ws.data_ptr() : nullptr, bytes, stream(dev));
+        if (st != AC_OK) return error(st);
+        PyObject *r = PyTuple_New(3);
+        if (!r) return nullptr;
+        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(dq));
+        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(dk));
+        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(dv));
+        return r;
+    }
+    CATCH
+}
+
 // The tensors of a cache: k, v, k_scale, v_scale.
 bool cache_of(PyObject *const *args, c10::DeviceIndex dev, ac_cache8 *c) {
     const Tensor *t[4];
@@ -256,6 +301,7 @@ PyObject *cache_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, nullptr},
     {"window", (PyCFunction)(void (*)(void))window, METH_FASTCALL, nullptr},
+    {"backward", (PyCFunction)(void (*)(void))backward, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"cache_attn", (PyCFunction)(void (*)(void))cache_attn, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

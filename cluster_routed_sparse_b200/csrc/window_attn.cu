@@ -181,7 +181,16 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
     float4 *grp_s = reinterpret_cast<float4 *>(sm + LY::OFF_GRP);
 
-    if (tid == 0) {
+    // K and V tiles j of the producer thread
+    auto load_tile = [&](bool v, int j) {
+        const int s = j % NS;
+        const uint32_t bar = BAR((v ? B_VF : B_KF) + s);
+        mbar_arrive_expect_tx(bar, LY::TILE);
+        for (int hf = 0; hf < LY::HALVES; ++hf)
+            tma_load_4d(sbase + (v ? LY::OFF_V : LY::OFF_K) + s * LY::TILE + hf * BN * 128, v ? &maps.v : &maps.k, hf * 64,
+                        tile_base(j), hk, b, bar);
+    };
+    if (tid == 8 * 32) {  // (the producer, so that the first loads start before the other warps are there)
         for (int i = 0; i < NS; ++i) {
             mbar_init(BAR(B_KF + i), C8 ? kConverters : 1);
             mbar_init(BAR(B_KE + i), 1);
@@ -199,7 +208,18 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         mbar_init(BAR(B_VZ), 1);
         mbar_init(BAR(B_QC), has1 ? 2 * BM : BM);
         fence_mbar_init();
+        if (n_tiles > 0) {
+            const uint32_t bytes = LY::HALVES * p.G * p.TT * 128;
+            mbar_arrive_expect_tx(BAR(B_QF), (has1 ? 2 : 1) * bytes);
+            for (int t = 0; t < (has1 ? 2 : 1); ++t)
+                for (int hf = 0; hf < LY::HALVES; ++hf)
+                    tma_load_5d(sbase + LY::OFF_Q + t * LY::TILE + hf * BM * 128, &maps.q, hf * 64, 0, i0 + t * p.TT, hk, b,
+                                BAR(B_QF));
+            if (!C8)
+                for (int j = 0; j < NS && j < n_tiles; ++j) load_tile(false, j), load_tile(true, j);
+        }
     }
+    __syncwarp();
     if (warp == 9) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -366,27 +386,16 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             }
             __syncwarp();
         } else if (warp == 8 && lane == 0 && n_tiles > 0) {
-            // ------------------------------------------------ query tiles
-            const uint32_t bytes = LY::HALVES * p.G * p.TT * 128;
-            mbar_arrive_expect_tx(BAR(B_QF), (has1 ? 2 : 1) * bytes);
-            for (int t = 0; t < (has1 ? 2 : 1); ++t)
-                for (int hf = 0; hf < LY::HALVES; ++hf)
-                    tma_load_5d(sbase + LY::OFF_Q + t * LY::TILE + hf * BM * 128, &maps.q, hf * 64, 0, i0 + t * p.TT, hk, b,
-                                BAR(B_QF));
             if (!C8) {
                 // -------------------------------------------- K/V producer
-                int kd = 0, vd = 0;
-                for (int j = 0; j < n_tiles; ++j) {
-                    const int s = j % NS, base = tile_base(j);
-                    if (j >= NS && !(ok = wait(BAR(B_KE + s), ((j / NS) - 1) & 1))) break;
-                    mbar_arrive_expect_tx(BAR(B_KF + s), LY::TILE);
-                    for (int hf = 0; hf < LY::HALVES; ++hf)
-                        tma_load_4d(sbase + LY::OFF_K + s * LY::TILE + hf * BN * 128, &maps.k, hf * 64, base, hk, b, BAR(B_KF + s));
+                int kd = min(NS, n_tiles), vd = kd;
+                for (int j = NS; j < n_tiles; ++j) {
+                    const int s = j % NS;
+                    if (!(ok = wait(BAR(B_KE + s), ((j / NS) - 1) & 1))) break;
+                    load_tile(false, j);
                     ++kd;
-                    if (j >= NS && !(ok = wait(BAR(B_VE + s), ((j / NS) - 1) & 1))) break;
-                    mbar_arrive_expect_tx(BAR(B_VF + s), LY::TILE);
-                    for (int hf = 0; hf < LY::HALVES; ++hf)
-                        tma_load_4d(sbase + LY::OFF_V + s * LY::TILE + hf * BN * 128, &maps.v, hf * 64, base, hk, b, BAR(B_VF + s));
+                    if (!(ok = wait(BAR(B_VE + s), ((j / NS) - 1) & 1))) break;
+                    load_tile(true, j);
                     ++vd;
                 }
                 // Loads still in flight must land before the CTA exits.
@@ -709,7 +718,7 @@ Plan plan(const WinArgs &a) {
     pl.nsplit = 1;
     double best = 1e30;
     for (int s = 1; s <= 64 && s <= std::max<int64_t>(n, 1); ++s) {
-        const double t = (double)((ctas * s + 147) / 148) * ((n + s - 1) / s + 4) * (a.k8 ? 2.6 : 1.9) + (s > 1 ? 2.5 + rows_us * s : 0.0);
+        const double t = (double)((ctas * s + 147) / 148) * ((n + s - 1) / s + 4) * (a.k8 ? 2.6 : 1.9) + (s > 1 ? 4.0 + rows_us * s : 0.0);
         if (t < best) best = t, pl.nsplit = s;
     }
     return pl;

@@ -231,7 +231,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
 
-    if (tid == 0) {
+    const int packed = p.G * p.TT;  // rows of a query tile
+    const uint32_t qbytes = LY::HALVES * packed * 128;
+    // L0 (t = 0, with the statistics of its queries) or L1 tile j, by the producer thread
+    auto load_tile = [&](int t, int j) {
+        const int s = j & 1, base = tile_base(j);
+        const uint32_t bar = BAR((t ? B_1F : B_0F) + s);
+        mbar_arrive_expect_tx(bar, (KEYS ? qbytes : LY::TILE) + (KEYS && t == 0 ? kStats * 4 : 0));
+        for (int hf = 0; hf < LY::HALVES; ++hf) {
+            const uint32_t dst = sbase + (t ? LY::OFF_L1 : LY::OFF_L0) + s * LY::TILE + hf * 128 * 128;
+            if (KEYS) tma_load_5d(dst, t ? &maps.l1 : &maps.l0, hf * 64, 0, base, hk, b, bar);
+            else tma_load_4d(dst, t ? &maps.l1 : &maps.l0, hf * 64, base, hk, b, bar);
+        }
+        if (KEYS && t == 0)
+            bulk_load(sbase + LY::OFF_ST + s * kStats * 4, p.stats + ((int64_t)bh * p.tiles_q + lo_c + j) * kStats, kStats * 4, bar);
+    };
+    if (tid == 8 * 32) {  // (the producer, so that the first loads start before the other warps are there)
         mbar_init(BAR(B_FF), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(BAR(B_0F + i), 1);
@@ -249,8 +264,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         mbar_init(BAR(B_Z1), 1);
         mbar_init(BAR(B_AF), 1);
         fence_mbar_init();
+        if (n_tiles > 0) {
+            mbar_arrive_expect_tx(BAR(B_FF), 2 * (KEYS ? LY::TILE : qbytes));
+            for (int t = 0; t < 2; ++t)
+                for (int hf = 0; hf < LY::HALVES; ++hf) {
+                    const uint32_t dst = sbase + LY::OFF_F + t * LY::TILE + hf * 128 * 128;
+                    if (KEYS) tma_load_4d(dst, t ? &maps.f1 : &maps.f0, hf * 64, r0, hk, b, BAR(B_FF));
+                    else tma_load_5d(dst, t ? &maps.f1 : &maps.f0, hf * 64, 0, r0, hk, b, BAR(B_FF));
+                }
+            for (int j = 0; j < 2 && j < n_tiles; ++j) load_tile(0, j), load_tile(1, j);
+        }
     }
-    const int packed = p.G * p.TT;  // rows of a query tile
+    __syncwarp();
     if (KEYS && packed < 128) {
         // The rows of the query stages that no load fills enter products over
         // the rows: zeros.
@@ -340,29 +365,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         } else if (warp == 8 && n_tiles > 0) {
           if (lane == 0) {
             // ------------------------------------------------ TMA producer
-            const uint32_t qbytes = LY::HALVES * packed * 128;
-            mbar_arrive_expect_tx(BAR(B_FF), 2 * (KEYS ? LY::TILE : qbytes));
-            for (int t = 0; t < 2; ++t)
-                for (int hf = 0; hf < LY::HALVES; ++hf) {
-                    const uint32_t dst = sbase + LY::OFF_F + t * LY::TILE + hf * 128 * 128;
-                    if (KEYS) tma_load_4d(dst, t ? &maps.f1 : &maps.f0, hf * 64, r0, hk, b, BAR(B_FF));
-                    else tma_load_5d(dst, t ? &maps.f1 : &maps.f0, hf * 64, 0, r0, hk, b, BAR(B_FF));
-                }
-            int done[2] = {0, 0};
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int s = j & 1, base = tile_base(j);
+            int done[2] = {min(2, n_tiles), min(2, n_tiles)};
+            for (int j = 2; j < n_tiles && ok; ++j) {
                 for (int t = 0; t < 2; ++t) {
-                    if (j >= 2 && !(ok = wait(BAR((t ? B_1E : B_0E) + s), ((j >> 1) - 1) & 1))) break;
-                    const uint32_t bar = BAR((t ? B_1F : B_0F) + s);
-                    mbar_arrive_expect_tx(bar, (KEYS ? qbytes : LY::TILE) + (KEYS && t == 0 ? kStats * 4 : 0));
-                    for (int hf = 0; hf < LY::HALVES; ++hf) {
-                        const uint32_t dst = sbase + (t ? LY::OFF_L1 : LY::OFF_L0) + s * LY::TILE + hf * 128 * 128;
-                        if (KEYS) tma_load_5d(dst, t ? &maps.l1 : &maps.l0, hf * 64, 0, base, hk, b, bar);
-                        else tma_load_4d(dst, t ? &maps.l1 : &maps.l0, hf * 64, base, hk, b, bar);
-                    }
-                    if (KEYS && t == 0)
-                        bulk_load(sbase + LY::OFF_ST + s * kStats * 4, p.stats + ((int64_t)bh * p.tiles_q + lo_c + j) * kStats,
-                                  kStats * 4, bar);
+                    if (!(ok = wait(BAR((t ? B_1E : B_0E) + (j & 1)), ((j >> 1) - 1) & 1))) break;
+                    load_tile(t, j);
                     ++done[t];
                 }
             }

@@ -229,6 +229,10 @@ def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int =
     """Gradients (dq, dk, dv) of window_attn with the same window and lengths, from
     d_out, the gradient of o, and the o and lse that it returned
     (ac_window_attn_backward).  out: (dq, dk, dv) to write into."""
+    if _fast is not None and out is None:
+        r = _fast.backward(d_out, q, k, v, o, lse, left, right, sinks, block, float(scale), q_lens, k_lens)
+        if _took(r):
+            return r
     dev = q.device
     qs = _shape(q, "q")
     B, Hq, Lq, d = qs
