@@ -28,7 +28,10 @@ __global__ void __launch_bounds__(kThreads, NC > 4 ? 3 : 6) k_cache8_append(cons
     const int h = idx % (uint32_t)a.Hk, b = idx / (uint32_t)a.Hk;
     const int start = a.start[b];
     int n = a.n;
-    if (a.counts) n = min(max(a.counts[b], 0), a.n);
+    if (a.counts) {
+        n = min(max(a.counts[b], 0), a.n);
+        if (n != a.counts[b] && threadIdx.x == 0) atomicOr(&a.err->bits, DEV_ERR_BOUNDS);
+    }
     if (start < 0) {
         if (threadIdx.x == 0) atomicOr(&a.err->bits, DEV_ERR_BOUNDS);
         return;

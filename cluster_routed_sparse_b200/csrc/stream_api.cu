@@ -142,6 +142,9 @@ extern "C" ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view
         a.x[t] = a.H[t] ? view_of(in) : View{};
         a.y[t] = a.H[t] ? view_of(out) : View{};
     }
+    for (int t = 0; t < 2; ++t)
+        if ((B > 1 && a.H[t] && !a.y[t].b) || (a.H[t] > 1 && !a.y[t].h) || (L > 1 && a.H[t] && !a.y[t].l))
+            return refuse("ac_rope_axes: an output cannot be a broadcast tensor");
     a.B = B, a.L = L, a.d = d;
     a.pos = positions, a.pos_b = pos_stride_b, a.n_axes = n_axes;
     a.interleaved = interleaved != 0, a.inverse = inverse != 0;

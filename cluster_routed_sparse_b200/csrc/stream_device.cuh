@@ -51,19 +51,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int3
         : "memory");
 }
 
-// Whether the phase with the given parity is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // ------------------------------------------------------------------ products
 // The issuing warp stays converged and its descriptors are the same in every
 // lane, so that they live in uniform registers; one elected lane executes the
@@ -76,16 +63,6 @@ __device__ __forceinline__ uint32_t elect_one() {
     return e;
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-
-// 32 lanes x 16 consecutive 32-bit columns from registers (thread i -> lane base + i).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 
 struct Desc {  // shared-memory matrix descriptor; offsets in 16-byte units stay within the low word
     uint32_t lo, hi;

@@ -354,21 +354,15 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     if (two) issue_s(1, 0);
                     commit(leader, BAR(B_KE));
                 }
-                bool there = false;  // V(j) and K(j + 1) are known to be there
                 for (int j = 0; j < n && go; ++j) {
                     const bool more = j + 1 < n;
-                    if (!there && !(go = wait_all(B_VF + j % NS, (j / NS) & 1) &&
-                                         (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
+                    // V and the next K are there long before P
+                    if (!(go = wait_all(B_VF + j % NS, (j / NS) & 1) && (!clean || more || wait_all(B_VZ, 0)) &&
+                               (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
                         break;
-                    if (clean && !more && !(go = wait_all(B_VZ, 0))) break;
                     for (int i = 0; i < (two ? 2 : 1); ++i) {
                         for (int hh = 0; hh < 2 && go; ++hh) {
                             const int h = hh ^ FIRST_HALF;
-                            // The last half of P is waited for longest: time to ask for what the next
-                            // iteration reads (a wait costs 150 cycles even when it is over).
-                            if (i == (two ? 1 : 0) && hh == 1)
-                                there = more && __all_sync(0xFFFFFFFFu, mbar_test(BAR(B_VF + (j + 1) % NS), ((j + 1) / NS) & 1) &&
-                                                                            (j + 2 >= n || mbar_test(BAR(B_KF + j % NS), ((j + 2) / NS) & 1)));
                             if (!(go = wait_all(B_PF + 2 * i + h, j & 1))) break;
                             tc_fence_after();
                             issue_pv(i, j, h);
@@ -452,7 +446,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
                 }
-                const int ex = min(max((int)(top >> 7) - 127, -120), 120);
+                const int ex = top ? min(max((int)(top >> 7) - 127, -120), 120) : 0;
                 const float dn = exp2i(-ex);
                 sl2 *= exp2i(ex);
 #pragma unroll 4
@@ -487,11 +481,12 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 // too, the first 64 are read again for the exponentials.
                 constexpr int KEEP = C8 ? 1 : 2;
                 uint32_t r[KEEP][2][32];
-                auto read = [&](int h) {
+                auto load = [&](int h) {
+                    tmem_ld32(tS + h * 64, r[h % KEEP][0]);
+                    tmem_ld32(tS + h * 64 + 32, r[h % KEEP][1]);
+                };
+                auto mask = [&](int h) {
                     uint32_t(&x)[2][32] = r[h % KEEP];
-                    tmem_ld32(tS + h * 64, x[0]);
-                    tmem_ld32(tS + h * 64 + 32, x[1]);
-                    tmem_ld_wait();
                     if (masked) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -503,6 +498,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     }
                 };
                 const float4 *grp = grp_s + (j & 3) * 8;  // of 16 keys each (over the cache)
+                // (never 0: a masked column is -inf times it)
+                auto factor = [&](float ks) { return fmaxf(sl2 * ks, 1e-37f); };
                 float m_new = m_run;
                 auto maximum = [&](int h) {
                     const uint32_t(&x)[2][32] = r[h % KEEP];
@@ -521,18 +518,22 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
 #pragma unroll
                         for (int a = 0; a < 64 / (C8 ? GROUP : 64); ++a) {
                             const float4 f = grp[h * 4 + a * (GROUP / 16)];
-                            m_new = fmaxf(m_new, fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), sl2 * f.x, f.y));
+                            m_new = fmaxf(m_new, fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), factor(f.x), f.y));
                         }
                     }
                 };
                 if (C8) {
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        read(h);
+                        load(h);
+                        tmem_ld_wait();
+                        mask(h);
                         maximum(h);
                     }
                 } else {
-                    read(0), read(1);
+                    load(0), load(1);
+                    tmem_ld_wait();
+                    mask(0), mask(1);
                     maximum(0), maximum(1);
                 }
                 // The rescale touches TMEM with warp-collective loads and stores, so
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                         for (int e = 0; e < 32; e += 2) {
                             if (C8 && e % (C8 ? GROUP : 32) == 0) {
                                 const float4 f = grp[h * 4 + 2 * c + e / 16];
-                                const float k = sl2 * f.x, n = f.y - m_use;
+                                const float k = factor(f.x), n = f.y - m_use;
                                 sl2x2 = f2_pack(k, k), negm2 = f2_pack(n, n);
                             }
                             const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sl2x2, negm2);
@@ -600,7 +601,11 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 if (C8) {
 #pragma unroll 1
                     for (int h = FIRST_HALF; h >= 0; --h) {
-                        if (h != FIRST_HALF) read(h);
+                        if (h != FIRST_HALF) {
+                            load(h);
+                            tmem_ld_wait();
+                            mask(h);
+                        }
                         weights(h);
                     }
                 } else {

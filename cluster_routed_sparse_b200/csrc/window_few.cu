@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
             for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const int ex = min(max((int)(top >> 7) - 127, -120), 120);  // |q| < 2^(ex + 1)
+            const int ex = top ? min(max((int)(top >> 7) - 127, -120), 120) : 0;  // |q| < 2^(ex + 1)
             g_c[rt] *= exp2i(ex);
             const float dn = exp2i(-ex);
 #pragma unroll

@@ -12,7 +12,8 @@ video generator that works frame after frame.
 Each call forwards data pointers, strides and the current stream of the
 tensors' device to the C ABI in include/ac.h, which documents the operators;
 all arithmetic runs in libac's kernels.  Tensors are [B, H, L, d] in any strides
-(d contiguous).  Nothing here synchronises but ops_status.
+(d contiguous).  Nothing here synchronises but ops_status, and nothing is
+recorded by autograd: gradients are calls of their own.
 
 The common case of a call (new outputs, tensors on the current device) goes
 through the compiled _fast module, which makes the same C calls; what it does

@@ -420,7 +420,8 @@ AC_API ac_status ac_state_import(ac_ctx *ctx, const void *host_buf, int64_t byte
  * of their own, may overlap.  Errors of arguments are returned at once
  * (ac_last_error_string(NULL) describes them); what only the device can see
  * (lengths, page indices, an expired wait) is clamped or left out there and
- * reported by the next ac_ops_status on that device.
+ * reported by the next ac_ops_status on that device (after an expired wait,
+ * call it before replaying the graph that the launch was captured in).
  *
  * ac_view: [B, H, L, d] elements, d contiguous, the other strides in elements
  * and free; the attention and the cache take bf16 rows on 16-byte boundaries
@@ -443,7 +444,8 @@ typedef enum ac_dtype { AC_DTYPE_BF16 = 0, AC_DTYPE_F16 = 1, AC_DTYPE_F32 = 2 } 
  * rotates back, which is also the gradient.  positions: device int32
  * [L, n_axes] for every sequence (pos_stride_b = 0) or per sequence
  * (pos_stride_b = entries from one to the next).  Angles are exact to 2^-32
- * turns at every position.  d even, at most 256; any strides.  y may be x itself.
+ * turns at every position.  d even, at most 256; any strides (an output's not 0).
+ * y may be x itself.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, d, device), CUDA. */
 AC_API ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view *y, int32_t H, const ac_view *x2,
                               const ac_view *y2, int32_t H2, int32_t B, int32_t L, int32_t d,

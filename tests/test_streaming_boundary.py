@@ -31,6 +31,7 @@ def rope(dtype=0, x=view(), y=view(), H=2, B=1, L=4, d=64, pos=A, freq=(1.0,) * 
     (dict(dtype=3), UNSUPPORTED), (dict(dtype=-1), UNSUPPORTED), (dict(d=63), UNSUPPORTED), (dict(d=258), UNSUPPORTED),
     (dict(pairs=(33,), freq=(1.0,) * 33), INVALID), (dict(pairs=(-1,)), INVALID), (dict(n_axes=0), INVALID),
     (dict(freq=(float("nan"),) * 32), INVALID), (dict(x=None), INVALID), (dict(y=view(p=None)), INVALID),
+    (dict(y=view(h=0)), INVALID), (dict(y=view(l=0)), INVALID), (dict(B=2, y=view(b=0)), INVALID),
     (dict(pos=None), INVALID), (dict(B=-1), INVALID), (dict(H=70000), INVALID),
 ])
 def test_rope_refusals(kw, expect):

@@ -433,6 +433,71 @@ def test_cache8_attn_scales_of_very_different_size(Lq):
         assert not o[:, 1].any()
 
 
+@pytest.mark.parametrize("T", [16, 64])
+@pytest.mark.parametrize("Lq", [2, 40])
+def test_cache8_attn_of_zeros(T, Lq):
+    """Queries of zeros over pages of zeros, with masked keys: the plain mean of the values, no NaN."""
+    g = gen(71)
+    c = crs.Cache8.empty(20, 1, T, 64)
+    table = torch.arange(20, device="cuda", dtype=torch.int32).view(1, 20)
+    lens = torch.tensor([T * 5 + 3], device="cuda", dtype=torch.int32)
+    v = normal(g, 1, 1, T * 5 + 3, 64)
+    crs.cache8_append(torch.zeros_like(v), v, c, table, torch.zeros_like(lens))
+    q = torch.zeros(1, 1, Lq, 64, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 1::2] = 2.0 ** -126
+    w = dict(left=T + 5, sinks=3)
+    o, lse = crs.cache8_attn(q, c, table, lens, return_lse=True, **w)
+    kk, vv = dense(c, table, T * 5 + 3)
+    r = ref.attention(q, kk, vv, ref.visible(1, Lq, T * 5 + 3, T + 5, 0, 3, 1))
+    ref.check("o", o, r)
+    ref.check("lse", lse, r)
+
+
+def test_counts_out_of_range_are_reported():
+    c = crs.Cache8.empty(4, 1, 16, 64)
+    k = normal(gen(72), 1, 1, 5, 64)
+    table = torch.arange(4, device="cuda", dtype=torch.int32).view(1, 4)
+    zero = torch.zeros(1, device="cuda", dtype=torch.int32)
+    for n, held in ((6, 5), (-1, 0)):
+        c.k.zero_()
+        crs.cache8_append(k, k, c, table, zero, zero + n)
+        with pytest.raises(_lib.ACError):
+            crs.ops_status()
+        assert int((c.k[0, 0].float().abs().sum(1) > 0).sum()) == held
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of more than 2^31 codes, and keys of more than 2^31 elements: the far end is read and written."""
+    g = gen(73)
+    pages, H, T, d = 17000, 8, 128, 128
+    c = crs.Cache8.empty(pages, H, T, d)
+    far = torch.tensor([[pages - 1, 3, pages - 2]], device="cuda", dtype=torch.int32)
+    k, v = normal(g, 1, H, 300, d), normal(g, 1, H, 300, d)
+    zero = torch.zeros(1, device="cuda", dtype=torch.int32)
+    crs.cache8_append(k, v, c, far, zero)
+    kk, vv = dense(c, far, 300)
+    for Lq in (1, 40):
+        q = normal(g, 1, H, Lq, d)
+        o = crs.cache8_attn(q, c, far, zero + 300)
+        ref.check("o", o, ref.attention(q, kk, vv, ref.visible(1, Lq, 300, -1, 0, 0, 1)))
+    assert float((kk - k.float()).norm() / k.float().norm()) < 2.0 ** -4
+    crs.ops_status()
+    del c, kk, vv
+    L = 2**31 // (H * d) + 1000
+    k = torch.zeros(1, H, L, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros_like(k)
+    k[:, :, -500:], v[:, :, -500:] = normal(g, 1, H, 500, d), normal(g, 1, H, 500, d)
+    for Lq in (1, 300):
+        q = normal(g, 1, H, Lq, d)
+        o, lse = crs.window_attn(q, k, v, left=150, return_lse=True)
+        r = ref.attention(q, k[:, :, -500:], v[:, :, -500:], ref.visible(1, Lq, 500, 150, 0, 0, 1), d_out=q)
+        ref.check("o", o, r)
+    dq, dk, dv = crs.window_attn_backward(q, q, k, v, o, lse, left=150)
+    for name, x in (("dq", dq), ("dk", dk[:, :, -500:]), ("dv", dv[:, :, -500:])):
+        ref.check(name, x, r)
+    assert not dk[:, :, :-500].any() and not dv[:, :, :-500].any()
+
+
 # ------------------------------------------------------------------ together
 def test_streaming_generation_and_training_step():
     """Frame after frame: rotate, attend within the window over the cache, append; the rotation and the window
