@@ -57,6 +57,14 @@ bool rows16(const ac_view *v, int B, int H, int L) {
     return true;
 }
 
+// Workspaces hold float4 parts and rows that bulk copies read.
+ac_status check_workspace(const char *what, const void *ws, int64_t bytes, int64_t need) {
+    if (need == 0) return AC_OK;
+    if (!ws || bytes < need) return refuse(what, AC_ERR_WORKSPACE);
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return refuse("the workspace must be 256-byte aligned");
+    return AC_OK;
+}
+
 ac_status window_rule(const ac_window *w, int d, WinRule *out, float *scale) {
     if (!w || w->left < -1 || w->right < -1 || w->sinks < 0 || w->block < 1 || !std::isfinite(w->scale) ||
         w->scale < 0.f)
@@ -182,8 +190,7 @@ extern "C" ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac
     if (B == 0 || Lq == 0) return AC_OK;
     if (!rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq) || (Lk > 0 && (!rows16(k, B, Hk, Lk) || !rows16(v, B, Hk, Lk))))
         return refuse("ac_window_attn: tensors must be 16-byte aligned with positive strides in multiples of 8");
-    if (workspace_bytes < need || (need && !workspace))
-        return refuse("ac_window_attn: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_workspace("ac_window_attn: workspace too small", workspace, workspace_bytes, need)) != AC_OK) return st;
     if ((st = check_device("ac_window_attn")) != AC_OK) return st;
     a.q = view_of(q), a.o = view_of(o);
     if (Lk > 0) a.k = view_of(k), a.v = view_of(v);
@@ -225,8 +232,7 @@ extern "C" ac_status ac_window_attn_backward(const ac_view *d_o, const ac_view *
                     !rows16(dq, B, Hq, Lq))) ||
         (Lk > 0 && (!rows16(k, B, Hk, Lk) || !rows16(v, B, Hk, Lk) || !rows16(dk, B, Hk, Lk) || !rows16(dv, B, Hk, Lk))))
         return refuse("ac_window_attn_backward: tensors must be 16-byte aligned with positive strides in multiples of 8");
-    if (workspace_bytes < need || (need && !workspace))
-        return refuse("ac_window_attn_backward: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_workspace("ac_window_attn_backward: workspace too small", workspace, workspace_bytes, need)) != AC_OK) return st;
     if ((st = check_device("ac_window_attn_backward")) != AC_OK) return st;
     if (Lq > 0) a.q = view_of(q), a.o = view_of(o), g.go = view_of(d_o), g.dq = view_of(dq);
     if (Lk > 0) a.k = view_of(k), a.v = view_of(v), g.dk = view_of(dk), g.dv = view_of(dv);
@@ -298,8 +304,7 @@ extern "C" ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, co
     if (!k_lens || (max_pages > 0 && !page_table)) return refuse("ac_cache8_attn: NULL page table or lengths");
     if (!rows16(q, B, Hq, Lq) || !rows16(o, B, Hq, Lq))
         return refuse("ac_cache8_attn: tensors must be 16-byte aligned with positive strides in multiples of 8");
-    if (workspace_bytes < need || (need && !workspace))
-        return refuse("ac_cache8_attn: workspace too small", AC_ERR_WORKSPACE);
+    if ((st = check_workspace("ac_cache8_attn: workspace too small", workspace, workspace_bytes, need)) != AC_OK) return st;
     if ((st = check_device("ac_cache8_attn")) != AC_OK) return st;
     WinArgs a{};
     if ((st = window_rule(w, cache->d, &a.w, &a.scale)) != AC_OK) return st;

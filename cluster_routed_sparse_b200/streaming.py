@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple
 
 import torch
@@ -127,12 +128,12 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
     the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
     fp32.  Returns (q, k) rotated, or q alone when k is None."""
-    pairs = tuple(pairs)
+    pairs = tuple(map(operator.index, pairs))
     axes = len(pairs)
     if freqs is not None:
-        freq, npairs, pf, pn = _axes_given(pairs, tuple(freqs))
+        freq, npairs, pf, pn = _axes_given(pairs, tuple(map(float, freqs)))
     else:
-        freq, npairs, pf, pn = _axes(pairs, tuple(theta) if isinstance(theta, (list, tuple)) else theta)
+        freq, npairs, pf, pn = _axes(pairs, tuple(map(float, theta)) if isinstance(theta, (list, tuple)) else float(theta))
     if _fast is not None and out is None:
         r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), 1 if interleaved else 0, 1 if inverse else 0)
         if _took(r):
@@ -167,6 +168,14 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
 
 
 # ---------------------------------------------------------------- window attention
+def _rule(left, right, sinks, block, scale):
+    """The window's numbers as what the C struct holds."""
+    n = tuple(map(operator.index, (left, right, sinks, block)))
+    if any(not -2 ** 31 <= x < 2 ** 31 for x in n):
+        raise ValueError(f"left, right, sinks and block must be 32-bit integers, got {n}")
+    return *n, float(scale)
+
+
 @functools.lru_cache(maxsize=1024)
 def _window(left, right, sinks, block, scale):
     return ACWindow(left, right, sinks, block, scale)
@@ -210,7 +219,7 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
         out = q.new_empty(shape)
     vo = _view(out, "out", dev, shape)
     lse = q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
-    w, n = _window_plan(left, right, sinks, block, scale, B, Hq, Hk, Lq, Lk, d)
+    w, n = _window_plan(*_rule(left, right, sinks, block, scale), B, Hq, Hk, Lq, Lk, d)
     ws = _workspace(n, q)
     _on(dev, _lib.load().ac_window_attn, vq, vk, vv, vo, _ptr(lse), B, Hq, Hk, Lq, Lk, d,
         _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n)
@@ -218,11 +227,12 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
 
 
 @functools.lru_cache(maxsize=1024)
-def _backward_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block):
+def _backward_plan(left, right, sinks, block, scale, *sizes):
+    """The window and the bytes of workspace of window_attn_backward at these sizes."""
     n = ctypes.c_int64(0)
-    check(_lib.load().ac_window_attn_backward_workspace(B, Hq, Hk, Lq, Lk, d, _window(left, right, sinks, block, 0.0),
-                                                        ctypes.byref(n)))
-    return n.value
+    w = _window(left, right, sinks, block, scale)
+    check(_lib.load().ac_window_attn_backward_workspace(*sizes, w, ctypes.byref(n)))
+    return w, n.value
 
 
 def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int = 0, sinks: int = 0, block: int = 1,
@@ -244,12 +254,11 @@ def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int =
     if lse.dtype is not torch.float32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be a contiguous fp32 tensor {(B, Hq, Lq)} on {dev}")
     dq, dk, dv = (q.new_empty(qs), q.new_empty(ks), q.new_empty(ks)) if out is None else out
-    n = _backward_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks, block)
+    w, n = _backward_plan(*_rule(left, right, sinks, block, scale), B, Hq, Hk, Lq, Lk, d)
     ws = _workspace(n, q)
     _on(dev, _lib.load().ac_window_attn_backward, vg, vq, vk, vv, vo, lse.data_ptr(), _view(dq, "dq", dev, qs),
         _view(dk, "dk", dev, ks), _view(dv, "dv", dev, ks), B, Hq, Hk, Lq, Lk, d,
-        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)),
-        _window(left, right, sinks, block, scale), _ptr(ws), n)
+        _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n)
     return dq, dk, dv
 
 
@@ -339,7 +348,7 @@ def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: 
     vo = _view(out, "out", dev, shape)
     lse = q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
     per = page_table.shape[1]
-    w, n = _cache_plan(left, right, sinks, block, scale, B, Hq, Lq, per, c.heads, c.page_tokens, d)
+    w, n = _cache_plan(*_rule(left, right, sinks, block, scale), B, Hq, Lq, per, c.heads, c.page_tokens, d)
     ws = _workspace(n, q)
     _on(dev, _lib.load().ac_cache8_attn, c, vq, vo, _ptr(lse), B, Hq, Lq, _ints(page_table, "page_table", dev, (B, per)), per,
         _ints(q_lens, "q_lens", dev, (B,)), _ints(k_lens, "k_lens", dev, (B,)), w, _ptr(ws), n)

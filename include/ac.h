@@ -470,7 +470,8 @@ typedef struct ac_window {
  * Lk).  A row that sees nothing, and a row behind its sequence, gets zeros and
  * lse = -inf; what the keys and values behind k_lens hold does not matter,
  * those before it must be finite.  lse: [B, Hq, Lq] fp32, natural logarithm,
- * nullable.  d 64 or 128, Hq / Hk at most 128.
+ * nullable.  d 64 or 128, Hq / Hk at most 128, B and Hq at most 65535, Lq and Lk
+ * at most 2^30, B Hq Lq and B Hk Lk at most 2^32.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 AC_API ac_status ac_window_attn_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk, int32_t d,
                                           const ac_window *w, int64_t *bytes);

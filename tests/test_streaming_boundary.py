@@ -132,3 +132,38 @@ def test_binding_refusals():
                  lambda: crs.rope_axes(x, x.float(), pos, (32,))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_workspaces_are_aligned():
+    assert backward(ws=A + 16) == INVALID
+    lib, n = _lib.load(), ctypes.c_int64(-1)
+    assert lib.ac_window_attn_workspace(1, 4, 2, 1, 1 << 20, 64, window(-1), ctypes.byref(n)) == 0 and n.value
+    assert attn(Lq=1, Lk=1 << 20, w=window(-1), ws=A + 128) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(left=2 ** 40), dict(left=2 ** 32 - 1), dict(right=2 ** 31), dict(sinks=2 ** 32 + 4),
+                                dict(block=2 ** 32 + 1)])
+def test_window_numbers_that_32_bits_do_not_hold(kw):
+    """Not taken modulo 2^32, which would be another window."""
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    lse, ints = torch.zeros(1, 2, 4), torch.zeros(1, 2, dtype=torch.int32)
+    for call in (lambda: crs.window_attn(x, x, x, **kw), lambda: crs.window_attn_backward(x, x, x, x, x, lse, **kw),
+                 lambda: crs.cache8_attn(x, crs.Cache8.empty(2, 2, 16, 64, "cpu"), ints, ints[0, :1], **kw)):
+        with pytest.raises(ValueError, match="32-bit"):
+            call()
+
+
+def test_rope_numbers_are_read_by_value():
+    """A tensor among them is read at the call, not remembered as an object."""
+    from cluster_routed_sparse_b200 import streaming
+    x, pos = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 1, dtype=torch.int32)
+    theta, pairs = torch.tensor(100.0), torch.tensor([32])
+    for _ in range(2):
+        streaming._axes.cache_clear()
+        with pytest.raises(ValueError, match="CUDA"):
+            crs.rope_axes(x, None, pos, pairs, theta)
+        before = streaming._axes.cache_info().misses
+        theta += 1
+        with pytest.raises(ValueError, match="CUDA"):
+            crs.rope_axes(x, None, pos, pairs, theta)
+        assert streaming._axes.cache_info().misses == before + 1
