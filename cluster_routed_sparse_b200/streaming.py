@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import numbers
 import operator
 from typing import NamedTuple
 
@@ -98,9 +99,17 @@ def _arrays(freq, pairs):
     return f, n, ctypes.addressof(f), ctypes.addressof(n)
 
 
+def _only(kind, *values):
+    """Remembered by value are numbers alone (a tensor would be remembered as an object)."""
+    if not all(isinstance(x, kind) for x in values):
+        raise TypeError(f"{kind.__name__} numbers expected")
+
+
 @functools.lru_cache(maxsize=64)
 def _axes(pairs, theta):
     """Frequencies of the pairs: axis i has the series theta^(-k / pairs[i]) of its own."""
+    _only(numbers.Integral, *pairs)
+    _only(numbers.Real, *(theta if isinstance(theta, tuple) else (theta,)))
     theta = (theta,) * len(pairs) if not isinstance(theta, tuple) else theta
     if len(theta) != len(pairs) or any(n < 0 for n in pairs) or any(not t > 0 for t in theta):
         raise ValueError("one theta > 0 for all axes, or one for each; pairs >= 0")
@@ -110,6 +119,8 @@ def _axes(pairs, theta):
 
 @functools.lru_cache(maxsize=64)
 def _axes_given(pairs, freqs):
+    _only(numbers.Integral, *pairs)
+    _only(numbers.Real, *freqs)
     if len(freqs) != sum(pairs):
         raise ValueError("one frequency for each pair")
     return _arrays(freqs, pairs)
@@ -128,12 +139,19 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
     the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
     fp32.  Returns (q, k) rotated, or q alone when k is None."""
-    pairs = tuple(map(operator.index, pairs))
+    pairs = tuple(pairs)
     axes = len(pairs)
-    if freqs is not None:
-        freq, npairs, pf, pn = _axes_given(pairs, tuple(map(float, freqs)))
-    else:
-        freq, npairs, pf, pn = _axes(pairs, tuple(map(float, theta)) if isinstance(theta, (list, tuple)) else float(theta))
+    try:
+        if freqs is not None:
+            freq, npairs, pf, pn = _axes_given(pairs, tuple(freqs))
+        else:
+            freq, npairs, pf, pn = _axes(pairs, tuple(theta) if isinstance(theta, (list, tuple)) else theta)
+    except TypeError:  # not plain numbers
+        pairs = tuple(map(operator.index, pairs))
+        if freqs is not None:
+            freq, npairs, pf, pn = _axes_given(pairs, tuple(map(float, freqs)))
+        else:
+            freq, npairs, pf, pn = _axes(pairs, tuple(map(float, theta)) if isinstance(theta, (list, tuple)) else float(theta))
     if _fast is not None and out is None:
         r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), 1 if interleaved else 0, 1 if inverse else 0)
         if _took(r):

@@ -158,12 +158,10 @@ def test_rope_numbers_are_read_by_value():
     from cluster_routed_sparse_b200 import streaming
     x, pos = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 1, dtype=torch.int32)
     theta, pairs = torch.tensor(100.0), torch.tensor([32])
-    for _ in range(2):
-        streaming._axes.cache_clear()
-        with pytest.raises(ValueError, match="CUDA"):
-            crs.rope_axes(x, None, pos, pairs, theta)
-        before = streaming._axes.cache_info().misses
+    streaming._axes.cache_clear()
+    for n in range(3):
         theta += 1
-        with pytest.raises(ValueError, match="CUDA"):
-            crs.rope_axes(x, None, pos, pairs, theta)
-        assert streaming._axes.cache_info().misses == before + 1
+        for _ in range(2):
+            with pytest.raises(ValueError, match="CUDA"):
+                crs.rope_axes(x, None, pos, pairs, theta)
+        assert streaming._axes.cache_info().currsize == n + 1
