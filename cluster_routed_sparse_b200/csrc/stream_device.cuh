@@ -51,6 +51,16 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int3
         : "memory");
 }
 
+// ------------------------------------------------------------------ chained launches
+// A kernel that launch_after started may begin while its predecessor's last CTAs run.
+// It waits here, until all of the predecessor is done and seen (the fence: by the bulk
+// loads too), before it touches what this call's kernels write.
+__device__ __forceinline__ void wait_predecessor() {
+    asm volatile("griddepcontrol.wait;\n\tfence.proxy.async;" ::: "memory");
+}
+// Lets the successor's CTAs take the SMs that are free once every CTA here has begun.
+__device__ __forceinline__ void release_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ products
 // The issuing warp stays converged and its descriptors are the same in every
 // lane, so that they live in uniform registers; one elected lane executes the

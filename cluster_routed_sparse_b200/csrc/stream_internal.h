@@ -18,6 +18,22 @@ struct OpErr {
 cudaError_t op_err_address(OpErr **out);
 uint32_t next_launch_id();
 
+// Launches a kernel of several that make up one call, never the first of them: it may
+// begin before the one in front of it has ended.  It reads the call's inputs at once,
+// and waits (wait_predecessor) before it touches anything that the call writes.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A &&...args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid, c.blockDim = dim3(block), c.dynamicSmemBytes = smem, c.stream = s;
+    c.attrs = &at, c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kern, P(args)...);
+    if (e == cudaSuccess) AC_NOTE_LAUNCH();
+    return e;
+}
+
 struct View {  // [B, H, L, d], d contiguous; strides in elements
     void *p;
     int64_t b, h, l;

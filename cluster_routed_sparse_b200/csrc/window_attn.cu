@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    release_successor();
     bool ok = true;
 
     if (C8 && warp >= 12) {
@@ -675,6 +676,7 @@ __global__ void __launch_bounds__(128) k_combine(const float *__restrict__ part_
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
+    wait_predecessor();
     float top = -INFINITY;
     for (int s = lane; s < nsplit; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
     for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
@@ -739,12 +741,8 @@ int64_t window_mma_workspace(const WinArgs &a) {
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Lq;
     const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (a.d == 128)
-        k_combine<128><<<grid, 128, 0, s>>>(part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
-    else
-        k_combine<64><<<grid, 128, 0, s>>>(part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
-    AC_NOTE_LAUNCH();
-    return cudaGetLastError();
+    auto kern = a.d == 128 ? k_combine<128> : k_combine<64>;
+    return launch_after(kern, grid, 128, 0, s, part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
 }
 
 cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s) {

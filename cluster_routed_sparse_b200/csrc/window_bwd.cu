@@ -128,6 +128,7 @@ __device__ __forceinline__ KeyTile key_tile(const BwdParams &p, int r0, int ql, 
 template <int D>
 __global__ void __launch_bounds__(256) k_row_stats(View go, View o, const float *__restrict__ lse, BwdParams p) {
     constexpr int LPR = D / 8;
+    release_successor();
     const int64_t idx = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
     const int part = threadIdx.x % LPR;
     const int row = (int)(idx % 128);
@@ -243,8 +244,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             if (KEYS) tma_load_5d(dst, t ? &maps.l1 : &maps.l0, hf * 64, 0, base, hk, b, bar);
             else tma_load_4d(dst, t ? &maps.l1 : &maps.l0, hf * 64, base, hk, b, bar);
         }
-        if (KEYS && t == 0)
-            bulk_load(sbase + LY::OFF_ST + s * kStats * 4, p.stats + ((int64_t)bh * p.tiles_q + lo_c + j) * kStats, kStats * 4, bar);
+    };
+    auto load_stats = [&](int j) {
+        const int s = j & 1;
+        bulk_load(sbase + LY::OFF_ST + s * kStats * 4, p.stats + ((int64_t)bh * p.tiles_q + lo_c + j) * kStats, kStats * 4, BAR(B_0F + s));
     };
     if (tid == 8 * 32) {  // (the producer, so that the first loads start before the other warps are there)
         mbar_init(BAR(B_FF), 1);
@@ -273,6 +276,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     else tma_load_5d(dst, t ? &maps.f1 : &maps.f0, hf * 64, 0, r0, hk, b, BAR(B_FF));
                 }
             for (int j = 0; j < 2 && j < n_tiles; ++j) load_tile(0, j), load_tile(1, j);
+            if (KEYS) {
+                wait_predecessor();
+                for (int j = 0; j < 2 && j < n_tiles; ++j) load_stats(j);
+            }
         }
     }
     __syncwarp();
@@ -293,6 +300,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    release_successor();
     constexpr uint32_t tS = 0, tP = 128, tA1 = 256, tA2 = 384;  // (all 512 columns are this CTA's: they start at 0)
     bool ok = true;
 
@@ -370,6 +378,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                 for (int t = 0; t < 2; ++t) {
                     if (!(ok = wait(BAR((t ? B_1E : B_0E) + (j & 1)), ((j >> 1) - 1) & 1))) break;
                     load_tile(t, j);
+                    if (KEYS && t == 0) load_stats(j);
                     ++done[t];
                 }
             }
@@ -410,6 +419,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         bool live;
         float nl = -INFINITY, delta = 0.f, rsum = 0.f;
         float *stat = p.stats + ((int64_t)bh * p.tiles_q + rt) * kStats;
+        wait_predecessor();
         if (KEYS) {
             live = r0 + row < kl;
             if (live) rr = key_range(p.w, r0 + row, off, ql, kl);
@@ -601,6 +611,7 @@ __global__ void __launch_bounds__(256) k_sum_parts(const BwdParams p) {
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
     const int parts = key_tile(p, r0, ql, kl).parts;
     if (parts == 1) return;
+    wait_predecessor();
     const float4 *src = reinterpret_cast<const float4 *>(p.parts + ((int64_t)bh * p.part_tiles + tile) * p.max_parts * 2 * 128 * D);
     for (int t = blockIdx.y * 256 + threadIdx.x; t < 2 * 128 * D / 4; t += gridDim.y * 256) {
         const int half = t / (128 * D / 4), row = t / (D / 4) % 128, e = t % (D / 4) * 4;
@@ -688,9 +699,13 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
         if (e != cudaSuccess || grid == 0) return;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return;
-        kern<<<(unsigned)grid, NTHREADS, smem, s>>>(m, p);
-        AC_NOTE_LAUNCH();
-        e = cudaGetLastError();
+        if (nq > 0) {
+            e = launch_after(kern, (unsigned)grid, NTHREADS, smem, s, m, p);
+        } else {  // the stream's previous kernel is not one of this call
+            kern<<<(unsigned)grid, NTHREADS, smem, s>>>(m, p);
+            AC_NOTE_LAUNCH();
+            e = cudaGetLastError();
+        }
     };
     if (nq > 0) {
         if (a.d == 128)
@@ -709,10 +724,7 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     }
     if (e == cudaSuccess && pt.part_tiles > 0) {
         const dim3 grid((unsigned)((int64_t)a.B * a.Hk * pt.part_tiles), 8);
-        if (a.d == 128) k_sum_parts<128><<<grid, 256, 0, s>>>(p);
-        else k_sum_parts<64><<<grid, 256, 0, s>>>(p);
-        AC_NOTE_LAUNCH();
-        e = cudaGetLastError();
+        e = launch_after(a.d == 128 ? k_sum_parts<128> : k_sum_parts<64>, grid, 256, 0, s, p);
     }
     return e;
 }

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
     constexpr int NR = 2 * RT;            // rows of a thread
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
 
+    release_successor();
     int idx = blockIdx.x;
     const int sp = idx % fp.nsplit;
     idx /= fp.nsplit;
