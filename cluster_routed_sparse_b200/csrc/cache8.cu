@@ -8,7 +8,11 @@
 // codes move by a power of two, exact except where they become subnormal.
 //
 // Bound by memory: 2 bytes read and 1 written per element.  One CTA holds one
-// (page, head, K or V) in registers: loads, page maximum, conversion, stores.
+// (page, head, K or V) in registers: loads, page maximum, conversion, stores; a page is
+// the unit because its scale needs all of it.  14,400 tokens of 40 heads, d = 128, pages
+// of 128 tokens (0.44 GB): 81 us, 5.5 TB/s, 84% of a copy (the loads of a page wait for
+// nothing, its stores for the maximum; 512 threads a page: no better).  One token of
+// eight sequences, 8 heads: 2.8 us in a graph.
 #include "stream_device.cuh"
 
 namespace ac {

@@ -36,8 +36,10 @@ ac_status check_device(const char *fn) {
 
 constexpr int kMaxLen = 1 << 30;
 
-// Few query rows for each key head are bound by reading the keys: they go to
-// the kernel whose products take 16 rows.
+// Few query rows for each key head are bound by reading the keys: up to 16 go to the
+// kernel whose products take that many.  (Us over 32,760 keys of 64 heads, d = 128, that
+// kernel against the tile kernel: 1 row 167 / 213 bf16, 99 / 298 in 8 bits; 8 rows 169 /
+// 213, 101 / 298; 16 rows 193 / 214, 188 / 299.  17 rows, on the tile kernel: 214, 299.)
 bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= 16; }
 int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {

@@ -41,6 +41,17 @@
 // Rounding: P to bf16 (fp16 over the cache), the operand type of the product,
 // 2^-9 (2^-12) relative and random over the keys; O once at the end; everything
 // else is fp32.
+// Bound by the softmax's chain: a pair of row tiles takes 3,500 cycles per key tile (S
+// 1,100 waited for, its load 150, maximum 320, exponentials 1,310, P 285, per row tile)
+// where the products take 2,048.  Frame-causal, 32,760 tokens in frames of 1,560, three
+// frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,070 us alone, 1.09 PFLOP/s, 65%
+// of the measured cuBLAS rate; 1,220 us in a long loop under the power limit.  A frame
+// of 1,560 over 18,720 cached tokens, 12 heads (0.18 TFLOP): 295 us, 36%; every CTA
+// converts the codes anew.  Dropped, in us of these two workloads: two threads a row
+// (1,266 in the loop; 595), a quarter of the exponentials as a polynomial on the FMA pipe
+// (no difference), a persistent CTA (1,059 against 1,028; 440 against 349 then), S in
+// 64-key halves that go round on their own (1,215 in the loop; 341).
+//
 // Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
 // issued and frees its TMEM.
 #include "stream_device.cuh"

@@ -16,9 +16,10 @@
 // times sum_j P_j k_j, would be the largest in dQ (1.2e-2 of its norm measured over
 // 5,000 keys, against 2e-3 from all other roundings).  Since sum_j dS_j = 0 for the
 // true delta, r = sum_j dS_j tells the error, and dQ = s (A2 - r A1) takes it
-// out; that is what A1 = P K is for.  r sums dS as rounded to bf16, so that the
-// part of those roundings which is common to all keys leaves too.  The second
-// role takes the corrected delta0 + r.
+// out; that is what A1 = P K is for.  There r sums dS as rounded to bf16, so that the
+// part of those roundings which is common to all keys leaves too.  The second role
+// takes delta0 plus the sum of dS before its rounding, which is the true delta (with
+// the rounded sum the error of dK is up to a fifth larger where rows see few keys).
 //
 // A key tile that many queries see (first tokens; early keys without a left bound)
 // would keep one SM busy after the others are done: its query tiles are split into
@@ -28,8 +29,22 @@
 // t mod 128, column half t / 128) turn S(j+1) into P while A2(j) and dP(j+1) run,
 // and dP into dS while A1(j+1) and S(j+2) run.  Tensor memory (512 columns):
 // S | dP | A1 | A2, each bf16 operand in the half of its scores that its own
-// threads have read; the products of each half start when its four warps are done.  P and dS are rounded to bf16 (the operand type), all
-// else is fp32.  Masks as in window_attn.cu: one column interval per thread.
+// threads have read; the products of each half start when its four warps are done.
+// P and dS are rounded to bf16, the operand type: 2^-8 of each at most and random over
+// the sum, so each gradient is as far off from that as from its own rounding to bf16
+// (2.3e-3 of its norm instead of 1.7e-3).  All else is fp32.  Masks as in
+// window_attn.cu: one column interval per thread.
+//
+// Bound by the tensor core and the hand-offs: 8 products of 128 x 128 x d per tile and
+// role pair, 3 more than one role with atomic sums into dQ would take, which is the
+// price of the same bits every time.  32,760 queries in frames of 1,560 over three
+// frames and the first, 12 heads, d = 128: 4.66 TFLOP in 4.0 ms, 1.16 PFLOP/s, 69% of
+// the measured cuBLAS rate; 2,830 cycles a tile in the first role and 3,000 in the
+// second where the products take 2,048 (the scores' wait 500, P 1,380, of which the
+// exponentials 1,024, dS 670, and in the second role the statistics 420).  Short loops
+// (clips) pay for their start: 4,800 cycles until the first tiles are there, a tile and
+// a half.  Dropped: P and dS in column halves of 64 that go round on their own (5,264
+// us with the forward, against 5,100); a barrier for each fixed tile (no difference).
 #include "stream_device.cuh"
 #include "stream_host.h"
 
@@ -49,8 +64,8 @@ struct Layout {
     static constexpr uint32_t OFF_L0 = 2 * TILE;       // [2] looped tiles
     static constexpr uint32_t OFF_L1 = OFF_L0 + 2 * TILE;
     static constexpr uint32_t OFF_ST = OFF_L1 + 2 * TILE;  // [2][kStats] statistics of the looped queries
-    static constexpr uint32_t OFF_R = OFF_ST + 2 * kStats * 4;  // [256] row sums
-    static constexpr uint32_t OFF_BAR = OFF_R + 256 * 4;
+    static constexpr uint32_t OFF_R = OFF_ST + 2 * kStats * 4;  // [2][256] row sums
+    static constexpr uint32_t OFF_BAR = OFF_R + 2 * 256 * 4;
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
 };
 
@@ -418,6 +433,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         int sink = 0;
         bool live;
         float nl = -INFINITY, delta = 0.f, rsum = 0.f;
+        uint64_t true_sum = f2_pack(0.f, 0.f);
         float *stat = p.stats + ((int64_t)bh * p.tiles_q + rt) * kStats;
         wait_predecessor();
         if (KEYS) {
@@ -504,16 +520,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                 for (int e = 0; e < 32; e += 4) {
                     float4 d4 = make_float4(delta, delta, delta, delta);
                     if (KEYS) d4 = *reinterpret_cast<const float4 *>(st + 128 + c * 32 + e);
+                    const uint64_t y01 = f2_mul(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])),
+                                                f2_sub(f2_pack(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), f2_pack(d4.x, d4.y)));
+                    const uint64_t y23 = f2_mul(f2_pack(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])),
+                                                f2_sub(f2_pack(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3])), f2_pack(d4.z, d4.w)));
                     float y[4];
-                    f2_unpack(f2_mul(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])),
-                                     f2_sub(f2_pack(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), f2_pack(d4.x, d4.y))), y[0], y[1]);
-                    f2_unpack(f2_mul(f2_pack(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])),
-                                     f2_sub(f2_pack(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3])), f2_pack(d4.z, d4.w))), y[2], y[3]);
+                    f2_unpack(y01, y[0], y[1]), f2_unpack(y23, y[2], y[3]);
                     const uint32_t w0 = pack_bf16x2(y[0], y[1]), w1 = pack_bf16x2(y[2], y[3]);
                     pk[c * 16 + e / 2] = w0, pk[c * 16 + e / 2 + 1] = w1;
-                    if (!KEYS)
+                    if (!KEYS) {
                         rsum += (__uint_as_float(w0 << 16) + __uint_as_float(w0 & 0xFFFF0000u)) +
                                 (__uint_as_float(w1 << 16) + __uint_as_float(w1 & 0xFFFF0000u));
+                        true_sum = f2_add(true_sum, f2_add(y01, y23));
+                    }
                 }
             }
             tmem_st32(mP, pk);
@@ -525,10 +544,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
         if (ok && n_tiles > 0 && !__all_sync(0xFFFFFFFFu, wait(BAR(B_AF), 0))) ok = false;
         tc_fence_after();
         if (!KEYS) {
-            row_sum[tid] = rsum;
+            float t0, t1;
+            f2_unpack(true_sum, t0, t1);
+            row_sum[tid] = rsum, row_sum[256 + tid] = t0 + t1;
             asm volatile("bar.sync 2, 256;" ::: "memory");
             rsum = row_sum[row] + row_sum[128 + row];
-            if (half == 0 && live && n_tiles > 0) stat[128 + row] = delta + rsum;
+            if (half == 0 && live && n_tiles > 0) stat[128 + row] = delta + (row_sum[256 + row] + row_sum[384 + row]);
         }
         const bool some = live && n_tiles > 0;
         if (KEYS) {
