@@ -36,11 +36,15 @@ ac_status check_device(const char *fn) {
 
 constexpr int kMaxLen = 1 << 30;
 
-// Few query rows for each key head are bound by reading the keys: up to 16 go to the
-// kernel whose products take that many.  (Us over 32,760 keys of 64 heads, d = 128, that
-// kernel against the tile kernel: 1 row 167 / 213 bf16, 99 / 298 in 8 bits; 8 rows 169 /
-// 213, 101 / 298; 16 rows 193 / 214, 188 / 299.  17 rows, on the tile kernel: 214, 299.)
-bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= 16; }
+// Few query rows for each key head are bound by reading the keys: up to 8 go to the
+// kernel whose products take that many, over the cache up to 16.  Us of that kernel
+// against the tile kernel, d = 128:
+//                                  1 row        8 rows       16 rows
+//   bf16   32,760 keys, 64 heads   167 / 165    169 / 166    192 / 167
+//          16,500 keys, 160 heads  206 / 230    211 / 232    257 / 235
+//           2,000 keys, 8 heads    10.1 / 13.7  10.6 / 13.4  12.5 / 13.5
+//   8 bits 32,760 keys, 64 heads    99 / 298    101 / 298    188 / 299
+bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= (a.k8 ? 16 : 8); }
 int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);

@@ -54,6 +54,8 @@
 //
 // Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
 // issued and frees its TMEM.
+#include <type_traits>
+
 #include "stream_device.cuh"
 #include "stream_host.h"
 
@@ -80,7 +82,8 @@ struct Layout {
     static constexpr uint32_t OFF_K = 2 * TILE;
     static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
     static constexpr uint32_t OFF_GRP = OFF_V + NS * TILE;  // [4][8] float4: a tile's groups of 16 keys (8-bit keys)
-    static constexpr uint32_t OFF_BAR = OFF_GRP + (C8 ? 4 * 8 * 16 : 0);
+    static constexpr uint32_t OFF_ROW = OFF_GRP + (C8 ? 4 * 8 * 16 : 0);  // [2][128] float2: maximum and sum of a row in each warpgroup
+    static constexpr uint32_t OFF_BAR = OFF_ROW + (C8 ? 0 : 2 * 128 * 8);
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // 1024-byte alignment slack
 };
 static_assert(Layout<128, 16>::SMEM <= 232448, "shared memory");
@@ -160,6 +163,12 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         hi_c = row_range(p.w, min(i0 + 2 * p.TT, ql) - 1 + off, kl).hi;
     }
     const bool has1 = i0 + p.TT < ql;
+    // One row tile alone: its key tiles go to the two warpgroups in turn, which are joined at the
+    // end.  (17 rows over 32,760 bf16 keys, 64 heads: 214 -> 167 us.  Not over the cache, where the
+    // code that this takes costs full pairs of tiles more than it gains: 299 -> 258 us, but a frame
+    // of 1,560 tokens 317 -> 332.)
+    const bool pair = C8 || has1;
+    const int step = pair ? 1 : 2;
     const int sink_c = min(p.w.sinks, hi_c);
     const int wt0 = lo_c / BN, wt1 = (hi_c + BN - 1) / BN;
     const int nsink = min((sink_c + BN - 1) / BN, wt0);
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         if (warp == 9) {
             // ------------------------------------------------ MMA issuer
             // (the whole warp, with the same values in every lane: see stream_device.cuh)
-            const int n = uniform(n_tiles), two = uniform(has1), clean = uniform(tail);
+            const int n = uniform(n_tiles), two = uniform(has1), solo = uniform(!pair), turn = solo ? 2 : 1, clean = uniform(tail);
             if (n > 0) {
                 constexpr uint32_t kTypes = C8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 or bf16 operands
                 constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false) & kTypes;
@@ -351,13 +360,13 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(BAR(bar), parity)) != 0; };
                 // (all 512 columns are this CTA's: tensor memory starts at address 0)
                 auto issue_s = [&](int i, int j) {
-                    mma_rows<D>(leader, i * BN, Desc{dq0.lo + i * STEP, dq0.hi}, Desc{dk0.lo + (j % NS) * STEP, dk0.hi}, IQK);
+                    mma_rows<D>(leader, i * BN, Desc{dq0.lo + (solo ? 0 : i) * STEP, dq0.hi}, Desc{dk0.lo + (j % NS) * STEP, dk0.hi}, IQK);
                     commit(leader, BAR(B_SF + i));
                 };
                 // the products of 64 keys, half h of P_i(j)
                 auto issue_pv = [&](int i, int j, int h) {
                     mma_weights<64>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV,
-                                    j > 0 || h != FIRST_HALF ? 1u : 0u, h);
+                                    j >= turn || h != FIRST_HALF ? 1u : 0u, h);
                 };
                 bool go = wait_all(C8 ? B_QC : B_QF, 0) && wait_all(B_KF, 0);
                 tc_fence_after();
@@ -366,25 +375,34 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     if (two) issue_s(1, 0);
                     commit(leader, BAR(B_KE));
                 }
+                if (go && solo && n > 1) {
+                    go = wait_all(B_KF + 1, 0);
+                    tc_fence_after();
+                    if (go) {
+                        issue_s(1, 1);
+                        commit(leader, BAR(B_KE + 1));
+                    }
+                }
                 for (int j = 0; j < n && go; ++j) {
-                    const bool more = j + 1 < n;
+                    const int next = j + turn;  // the tile whose scores take the place of tile j's weights
+                    const bool more = next < n;
                     // V and the next K are there long before P
-                    if (!(go = wait_all(B_VF + j % NS, (j / NS) & 1) && (!clean || more || wait_all(B_VZ, 0)) &&
-                               (!more || wait_all(B_KF + (j + 1) % NS, ((j + 1) / NS) & 1))))
+                    if (!(go = wait_all(B_VF + j % NS, (j / NS) & 1) && (!clean || j + 1 < n || wait_all(B_VZ, 0)) &&
+                               (!more || wait_all(B_KF + next % NS, (next / NS) & 1))))
                         break;
-                    for (int i = 0; i < (two ? 2 : 1); ++i) {
+                    for (int i = solo ? j & 1 : 0; i < (solo ? (j & 1) + 1 : two ? 2 : 1); ++i) {
                         for (int hh = 0; hh < 2 && go; ++hh) {
                             const int h = hh ^ FIRST_HALF;
-                            if (!(go = wait_all(B_PF + 2 * i + h, j & 1))) break;
+                            if (!(go = wait_all(B_PF + 2 * i + h, (solo ? j >> 1 : j) & 1))) break;
                             tc_fence_after();
                             issue_pv(i, j, h);
                         }
                         if (!go) break;
-                        if (more) issue_s(i, j + 1);
+                        if (more) issue_s(i, next);
                         else commit(leader, BAR(B_OF + i));
                     }
                     if (!go) break;
-                    if (more) commit(leader, BAR(B_KE + (j + 1) % NS));
+                    if (more) commit(leader, BAR(B_KE + next % NS));
                     commit(leader, BAR(B_VE + j % NS));
                 }
                 commit(leader, BAR(B_DONE));
@@ -395,14 +413,20 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             if (!C8) {
                 // -------------------------------------------- K/V producer
                 int kd = min(NS, n_tiles), vd = kd;
-                for (int j = NS; j < n_tiles; ++j) {
-                    const int s = j % NS;
-                    if (!(ok = wait(BAR(B_KE + s), ((j / NS) - 1) & 1))) break;
-                    load_tile(false, j);
-                    ++kd;
-                    if (!(ok = wait(BAR(B_VE + s), ((j / NS) - 1) & 1))) break;
-                    load_tile(true, j);
-                    ++vd;
+                // One row tile: K runs a tile ahead of V, because S is issued two tiles ahead of P V.
+                const int lag = step - 1;
+                for (int j = NS; j < n_tiles + lag; ++j) {
+                    if (j < n_tiles) {
+                        if (!(ok = wait(BAR(B_KE + j % NS), ((j / NS) - 1) & 1))) break;
+                        load_tile(false, j);
+                        ++kd;
+                    }
+                    const int jv = j - lag;
+                    if (jv >= NS) {
+                        if (!(ok = wait(BAR(B_VE + jv % NS), ((jv / NS) - 1) & 1))) break;
+                        load_tile(true, jv);
+                        ++vd;
+                    }
                 }
                 // Loads still in flight must land before the CTA exits.
                 for (int j = max(kd - NS, 0); j < kd; ++j) wait(BAR(B_KF + j % NS), (j / NS) & 1);
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         // ------------------------------------------------ softmax + epilogue
         const int wg = warp >> 2;
         const int row = tid & 127;
-        const int g = row % p.G, i = i0 + wg * p.TT + row / p.G;
+        const int g = row % p.G, i = i0 + (pair ? wg * p.TT : 0) + row / p.G;
         const bool mine = row < p.G * p.TT && i < p.Lq;
         const bool live = mine && i < ql;
         // A row that is not live computes something that is not used: it sees
@@ -443,7 +467,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + wg * BN;
         const uint32_t tO = tmem + lane_off + 256 + wg * 128;
-        const bool active = n_tiles > 0 && (wg == 0 || has1);
+        const bool active = C8 ? n_tiles > 0 && (wg == 0 || has1) : n_tiles > (has1 ? 0 : wg);
+        float2 *row_s = reinterpret_cast<float2 *>(sm + LY::OFF_ROW);
         if (active) {
             float sl2 = p.scale_log2;
             if (C8) {
@@ -474,13 +499,13 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(B_QC));
             }
-            for (int j = 0; j < n_tiles && ok; ++j) {
+            for (int j = pair ? 0 : wg; j < n_tiles && ok; j += step) {
                 // Wait outcomes are combined across the warp: the TMEM loads and
                 // stores below are warp-collective, so a warp leaves together.
                 // (Over the cache S also tells that the tile's groups are there: they were stored
                 // before K was, which S waited for.  A wait for K itself could miss its phase:
                 // K of tile j + 2 may be there already.)
-                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_SF + wg), j & 1))) {
+                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_SF + wg), (pair ? j : j >> 1) & 1))) {
                     ok = false;
                     break;
                 }
@@ -550,8 +575,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 }
                 // The rescale touches TMEM with warp-collective loads and stores, so
                 // the whole warp moves when one live row's maximum grew by more than 2^8.
-                if (__any_sync(0xFFFFFFFFu, j == 0 || (live && m_new > m_run + kRescaleLog2))) {
-                    if (j > 0) {
+                if (__any_sync(0xFFFFFFFFu, j < step || (live && m_new > m_run + kRescaleLog2))) {
+                    if (j >= step) {
                         const float alpha = m_new > m_run ? ex2_approx(m_run - m_new) : 1.f;
                         l_run *= alpha;
 #pragma unroll 1
@@ -626,12 +651,30 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             }
             if (ok && !__all_sync(0xFFFFFFFFu, wait(BAR(B_OF + wg), 0))) ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
-            tc_fence_after();
         }
-        const bool some = active && live && m_run > -INFINITY;
+        // (one row tile: each warpgroup reads both accumulators)
+        if (!pair && n_tiles > 1 - wg && ok && !__all_sync(0xFFFFFFFFu, wait(BAR(B_OF + 1 - wg), 0))) ok = false;
+        tc_fence_after();
+        // Columns [c0, c1) of 32 to store; one row tile: half each, of w0 O_0 + w1 O_1.
+        int c0 = 0, c1 = D / 32;
+        float w0 = 1.f, w1 = 0.f;
+        if (!pair) {
+            row_s[wg * 128 + row] = make_float2(ok ? m_run : NAN, l_run);
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            const float2 a = row_s[row], c = row_s[128 + row];
+            ok = ok && a.x == a.x && c.x == c.x;
+            m_run = fmaxf(a.x, c.x);
+            w0 = a.x > -INFINITY ? ex2_approx(a.x - m_run) : 0.f;
+            w1 = c.x > -INFINITY ? ex2_approx(c.x - m_run) : 0.f;
+            l_run = a.y * w0 + c.y * w1;
+            c0 = wg * (D / 64), c1 = c0 + D / 64;
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        const bool read = C8 ? active : n_tiles > 0;
+        const bool some = read && live && m_run > -INFINITY;
         const float il = some ? 1.f / l_run : 0.f;
         const int64_t orow = ((int64_t)b * p.Hq + hk * p.G + g) * p.Lq + i;
-        if (ok && mine) {
+        if (ok && mine && (pair || wg == 0)) {
             const float lse = some ? (m_run + __log2f(l_run)) * 0.693147180559945f : -INFINITY;
             if (p.nsplit > 1)
                 p.part_lse[(int64_t)sp * p.B * p.Hq * p.Lq + orow] = lse;
@@ -642,11 +685,20 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             float4 *dst4 = reinterpret_cast<float4 *>(p.part_o + ((int64_t)sp * p.B * p.Hq * p.Lq + orow) * D);
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.o.p) + b * p.o.b + (int64_t)(hk * p.G + g) * p.o.h + i * p.o.l);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 uint32_t o[32];
-                if (active) {
-                    tmem_ld32(tO + c * 32, o);
+                if (read) {
+                    tmem_ld32((pair ? tO : tmem + lane_off + 256) + c * 32, o);
                     tmem_ld_wait();
+                }
+                if (!pair && read) {
+                    uint32_t o1[32];
+                    tmem_ld32(tmem + lane_off + 256 + 128 + c * 32, o1);
+                    tmem_ld_wait();
+                    // (what a warpgroup that saw nothing of the row left there does not count)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint((w0 > 0.f ? __uint_as_float(o[e]) * w0 : 0.f) + (w1 > 0.f ? __uint_as_float(o1[e]) * w1 : 0.f));
                 }
                 if (mine && p.nsplit > 1) {
                     if (some) {
@@ -667,6 +719,20 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 }
             }
         }
+        if (!pair && wg == 1) {
+            // the rows of the second tile, all behind the sequence
+            const int i1 = i + p.TT;
+            if (row < p.G * p.TT && i1 < p.Lq) {
+                if (p.nsplit > 1) {
+                    p.part_lse[(int64_t)sp * p.B * p.Hq * p.Lq + orow + p.TT] = -INFINITY;
+                } else {
+                    if (p.lse) p.lse[orow + p.TT] = -INFINITY;
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.o.p) + b * p.o.b + (int64_t)(hk * p.G + g) * p.o.h + i1 * p.o.l);
+#pragma unroll 1
+                    for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
     }
 #undef BAR
     tc_fence_before();
@@ -677,35 +743,53 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     }
 }
 
-// Joins the partial results of a row: O = sum_s w_s O_s with w_s = 2^(lse_s - lse)
-// (natural logarithms).  A part that saw nothing has lse_s = -inf and no O_s.
-// One warp per row; bound by reading the partials once.
-template <int D>
+// Joins the partial results of a row: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  A
+// part that saw nothing has lse_s = -inf and no O_s.  WARPS warps per row, each over
+// every WARPS-th group of 32 parts; bound by the latency of the parts' loads, so that
+// many parts want several warps (one row, 390 parts: 83 us with one warp that read the
+// parts one after the other).
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) k_combine(const float *__restrict__ part_o, const float *__restrict__ part_lse,
                                                  View o, float *lse, int64_t rows, int nsplit, int Hq, int Lq) {
     constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
+    typedef typename std::conditional<N == 4, float4, float2>::type Vec;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % WARPS;
+    const int64_t row = (int64_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
+    if (row >= rows) return;  // (WARPS = 4: the whole block)
     wait_predecessor();
     float top = -INFINITY;
     for (int s = lane; s < nsplit; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
     for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     float acc[N] = {}, sum = 0.f;
     if (top > -INFINITY) {
-        for (int s = 0; s < nsplit; ++s) {
-            const float ls = part_lse[s * rows + row];
-            if (ls == -INFINITY) continue;
-            const float w = __expf(ls - top);
-            sum += w;
-            const float *src = part_o + (s * rows + row) * D + lane * N;
-            if constexpr (N == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(src);
-                acc[0] += w * f.x, acc[1] += w * f.y, acc[2] += w * f.z, acc[3] += w * f.w;
-            } else {
-                const float2 f = *reinterpret_cast<const float2 *>(src);
-                acc[0] += w * f.x, acc[1] += w * f.y;
+        const int len = WARPS == 1 ? 32 : 8;  // parts of a group
+        for (int s0 = w0 * len; s0 < nsplit; s0 += WARPS * len) {
+            const int n = min(len, nsplit - s0);
+            const float mine = lane < n ? __expf(part_lse[(s0 + lane) * rows + row] - top) : 0.f;
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xFFFFFFFFu, mine, i);
+                Vec f{};
+                if (w > 0.f) f = *reinterpret_cast<const Vec *>(part_o + ((s0 + i) * rows + row) * D + lane * N);
+                const float *x = reinterpret_cast<const float *>(&f);
+                sum += w;
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(w, x[e], acc[e]);
             }
+        }
+    }
+    if constexpr (WARPS > 1) {
+        __shared__ float s_acc[WARPS][D], s_sum[WARPS];
+#pragma unroll
+        for (int e = 0; e < N; ++e) s_acc[warp][lane * N + e] = acc[e];
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+            sum += s_sum[w];
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] += s_acc[w][lane * N + e];
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -751,8 +835,10 @@ int64_t window_mma_workspace(const WinArgs &a) {
 
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Lq;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    auto kern = a.d == 128 ? k_combine<128> : k_combine<64>;
+    // Several warps where there are more parts than one has loads in flight, and few rows.
+    const bool several = nsplit > 8 && rows <= 148 * 16;
+    const unsigned grid = (unsigned)(several ? rows : (rows + 3) / 4);
+    auto kern = a.d == 128 ? (several ? k_combine<128, 4> : k_combine<128, 1>) : several ? k_combine<64, 4> : k_combine<64, 1>;
     return launch_after(kern, grid, 128, 0, s, part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
 }
 

@@ -1,5 +1,5 @@
-// window_few.cu -- the same attention for few query rows: single tokens, or a
-// few, with G * Lq <= 16 rows for each key head, over bf16 keys or the 8-bit cache.
+// window_few.cu -- the same attention for few query rows: single tokens, or a few,
+// with G * Lq <= 8 rows for each key head over bf16 keys, <= 16 over the 8-bit cache.
 //
 // Bound by reading K and V once.  A warp takes 16 keys at a time, and the rows are
 // the short side of m16n8k16 products: S^T = K Q^T, the running softmax of
@@ -21,7 +21,7 @@
 // over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 93 us, 5.8 TB/s, 90% of it;
 // the rest is the joining launch and the last wave.  With 9 to 16 rows the registers
 // leave three CTAs on an SM and the loads in flight no longer cover their latency: 188
-// us over that cache, 193 over bf16 keys (the tile kernel: 299 and 214).
+// us over that cache.
 //
 // Types, scales and roundings as in the tile kernel: bf16 over bf16 keys, fp16 with
 // the scales in the exponents over the 8-bit cache.
@@ -73,7 +73,7 @@ __device__ __forceinline__ void load_bytes(uint32_t (&r)[BYTES / 4], const void 
     }
 }
 
-// RT: tiles of 8 rows (1 or 2).  One tile takes few enough registers for another CTA
+// RT: tiles of 8 rows (1, or 2 over the cache).  One tile takes few enough registers for another CTA
 // on the SM, hence more loads in flight.
 template <int D, bool C8, int RT>
 __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(const __grid_constant__ FewParams fp) {
@@ -410,10 +410,10 @@ cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s) {
     const bool half = (int64_t)a.G * a.Lq <= 8;
     if (a.d == 128) {
         if (a.k8) half ? go(k_window_few<128, true, 1>) : go(k_window_few<128, true, 2>);
-        else half ? go(k_window_few<128, false, 1>) : go(k_window_few<128, false, 2>);
+        else go(k_window_few<128, false, 1>);
     } else {
         if (a.k8) half ? go(k_window_few<64, true, 1>) : go(k_window_few<64, true, 2>);
-        else half ? go(k_window_few<64, false, 1>) : go(k_window_few<64, false, 2>);
+        else go(k_window_few<64, false, 1>);
     }
     AC_NOTE_LAUNCH();
     cudaError_t e = cudaGetLastError();

@@ -137,6 +137,9 @@ CASES = [
     (1, 128, 1, 2, 200, 64, -1, 0, 0, 1),
     (2, 40, 40, 300, 1100, 64, -1, 0, 0, 1),    # many tiles to a block, with padding in the last
     (1, 40, 40, 1000, 1300, 128, -1, 200, 0, 1),
+    (1, 2, 1, 3, 40000, 64, -1, 0, 0, 1),       # one head, many keys: many parts to join
+    (1, 1, 1, 1, 70001, 128, 65000, 0, 100, 1),
+    (1, 16, 1, 2, 9000, 128, -1, 0, 0, 1),
 ]
 
 
@@ -195,6 +198,47 @@ def test_window_attn_backward(case, ragged):
         ref.check(name, x, r)
     for a, b in zip((dq, dk, dv), crs.window_attn_backward(g, q, k, v, o, lse, **kw)):
         assert torch.equal(a, b)  # the same bits every time
+
+
+@pytest.mark.parametrize("cached", [False, True])
+@pytest.mark.parametrize("case", [
+    (4, 1, 1, 200, 2000, 128, -1, 0, 0, 1),
+    (4, 2, 2, 200, 900, 64, 300, 0, 130, 1),
+    (3, 5, 1, 13, 5000, 128, -1, -1, 0, 1),
+    (4, 8, 1, 20, 1300, 128, 200, 0, 40, 1),
+    (2, 1, 1, 30, 130, 64, 3, 3, 1, 1),
+    (40, 4, 4, 140, 700, 64, 500, 0, 100, 1),   # enough heads that no key is split off
+    (40, 4, 4, 100, 200, 128, -1, 50, 0, 1),
+])
+def test_one_tile_of_queries(case, cached):
+    """Sequences whose queries fill at most one row tile of two, and lengths that leave the other one,
+    or both, behind the sequence: those rows get zeros whatever the output held."""
+    B, Hq, Hk, Lq, Lk, d = case[:6]
+    q, k, v, _ = tensors(case, 3)
+    ints = dict(device="cuda", dtype=torch.int32)
+    q_lens = torch.tensor([(Lq, 5, 0, min(130, Lq))[b % 4] for b in range(B)], **ints)
+    k_lens = torch.tensor([(Lk, Lk - 7, 60, 129, 0)[b % 5] for b in range(B)], **ints)
+    out = torch.full_like(q, math.nan)
+    kw = dict(q_lens=q_lens, out=out, return_lse=True, **rule(case))
+    if cached:
+        T = 32
+        per = (Lk + T - 1) // T
+        c = crs.Cache8.empty(B * per, Hk, T, d)
+        table = torch.randperm(B * per, generator=gen(1), device="cuda").view(B, per).to(torch.int32)
+        crs.cache8_append(k, v, c, table, torch.zeros(B, **ints), k_lens)
+        o, lse = crs.cache8_attn(q, c, table, k_lens, **kw)
+        k, v = dense(c, table, Lk)
+        keep = torch.arange(Lk, device="cuda").view(1, 1, Lk, 1) < k_lens.view(B, 1, 1, 1)
+        k, v = torch.where(keep, k, 0.0), torch.where(keep, v, 0.0)
+    else:
+        for b in range(B):
+            k[b, :, int(k_lens[b]):] = math.nan
+            v[b, :, int(k_lens[b]):] = math.nan
+        o, lse = crs.window_attn(q, k, v, k_lens=k_lens, **kw)
+    crs.ops_status()
+    r = ref.attention(q, k, v, ref.visible(B, Lq, Lk, *case[6:], q_lens, k_lens))
+    ref.check("o", o, r)
+    ref.check("lse", lse, r)
 
 
 def test_window_attn_strided_views_and_scale():
