@@ -40,10 +40,10 @@ constexpr int kMaxLen = 1 << 30;
 // kernel whose products take that many, over the cache up to 16.  Us of that kernel
 // against the tile kernel, d = 128:
 //                                  1 row        8 rows       16 rows
-//   bf16   32,760 keys, 64 heads   167 / 165    169 / 166    192 / 167
-//          16,500 keys, 160 heads  206 / 230    211 / 232    257 / 235
-//           2,000 keys, 8 heads    10.1 / 13.7  10.6 / 13.4  12.5 / 13.5
-//   8 bits 32,760 keys, 64 heads    99 / 298    101 / 298    188 / 299
+//   bf16   32,760 keys, 64 heads   162 / 165    164 / 166    192 / 168
+//          16,500 keys, 160 heads  202 / 228    208 / 230    257 / 231
+//           2,000 keys, 8 heads    9.0 / 10.3   9.4 / 10.3   12.5 / 10.4
+//   8 bits 32,760 keys, 64 heads    97 / 296     99 / 296    186 / 297
 bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= (a.k8 ? 16 : 8); }
 int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {

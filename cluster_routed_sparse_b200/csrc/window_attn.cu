@@ -744,37 +744,36 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
 }
 
 // Joins the partial results of a row: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  A
-// part that saw nothing has lse_s = -inf and no O_s.  WARPS warps per row, each over
-// every WARPS-th group of 32 parts; bound by the latency of the parts' loads, so that
-// many parts want several warps (one row, 390 parts: 83 us with one warp that read the
-// parts one after the other).
+// part that saw nothing has lse_s = -inf and no O_s.  WARPS warps per row, each with the
+// loads of eight parts in flight; bound by their latency.  (One row of 100,000 keys, 390
+// parts: 101 us in all when one warp read the parts one after the other, 17 now.)
 template <int D, int WARPS>
-__global__ void __launch_bounds__(128) k_combine(const float *__restrict__ part_o, const float *__restrict__ part_lse,
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const float *__restrict__ part_o, const float *__restrict__ part_lse,
                                                  View o, float *lse, int64_t rows, int nsplit, int Hq, int Lq) {
     constexpr int N = D / 32;
     typedef typename std::conditional<N == 4, float4, float2>::type Vec;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % WARPS;
-    const int64_t row = (int64_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
-    if (row >= rows) return;  // (WARPS = 4: the whole block)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = WARPS == 1 ? 0 : warp;
+    const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
+    if (row >= rows) return;
     wait_predecessor();
     float top = -INFINITY;
     for (int s = lane; s < nsplit; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
     for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     float acc[N] = {}, sum = 0.f;
     if (top > -INFINITY) {
-        const int len = WARPS == 1 ? 32 : 8;  // parts of a group
-        for (int s0 = w0 * len; s0 < nsplit; s0 += WARPS * len) {
-            const int n = min(len, nsplit - s0);
+        for (int s0 = w0 * 8; s0 < nsplit; s0 += WARPS * 8) {
+            const int n = min(8, nsplit - s0);
             const float mine = lane < n ? __expf(part_lse[(s0 + lane) * rows + row] - top) : 0.f;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
+            Vec f[8];  // (loaded whatever it holds, so that all are in flight)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const Vec *>(part_o + ((s0 + min(i, n - 1)) * rows + row) * D + lane * N);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
                 const float w = __shfl_sync(0xFFFFFFFFu, mine, i);
-                Vec f{};
-                if (w > 0.f) f = *reinterpret_cast<const Vec *>(part_o + ((s0 + i) * rows + row) * D + lane * N);
-                const float *x = reinterpret_cast<const float *>(&f);
+                const float *x = reinterpret_cast<const float *>(&f[i]);
                 sum += w;
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+                for (int e = 0; e < N; ++e) acc[e] = w > 0.f ? fmaf(w, x[e], acc[e]) : acc[e];
             }
         }
     }
@@ -836,10 +835,10 @@ int64_t window_mma_workspace(const WinArgs &a) {
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Lq;
     // Several warps where there are more parts than one has loads in flight, and few rows.
-    const bool several = nsplit > 8 && rows <= 148 * 16;
+    const bool several = nsplit > 8 && rows <= 148 * 8;
     const unsigned grid = (unsigned)(several ? rows : (rows + 3) / 4);
-    auto kern = a.d == 128 ? (several ? k_combine<128, 4> : k_combine<128, 1>) : several ? k_combine<64, 4> : k_combine<64, 1>;
-    return launch_after(kern, grid, 128, 0, s, part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
+    auto kern = a.d == 128 ? (several ? k_combine<128, 8> : k_combine<128, 1>) : several ? k_combine<64, 8> : k_combine<64, 1>;
+    return launch_after(kern, grid, several ? 256 : 128, 0, s, part_o, part_lse, a.o, a.lse, rows, nsplit, a.Hq, a.Lq);
 }
 
 cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s) {
