@@ -36,15 +36,23 @@ ac_status check_device(const char *fn) {
 
 constexpr int kMaxLen = 1 << 30;
 
-// Few query rows for each key head are bound by reading the keys: up to 8 go to the
-// kernel whose products take that many, over the cache up to 16.  Us of that kernel
-// against the tile kernel, d = 128:
-//                                  1 row        8 rows       16 rows
-//   bf16   32,760 keys, 64 heads   162 / 165    164 / 166    192 / 168
-//          16,500 keys, 160 heads  202 / 228    208 / 230    257 / 231
-//           2,000 keys, 8 heads    9.0 / 10.3   9.4 / 10.3   12.5 / 10.4
-//   8 bits 32,760 keys, 64 heads    97 / 296     99 / 296    186 / 297
-bool few_rows(const WinArgs &a) { return (int64_t)a.G * a.Lq <= (a.k8 ? 16 : 8); }
+// Few query rows for each key head are bound by reading the keys: they go to the kernel
+// whose products take 8 rows.  It reads the keys once for every 8 rows, from the L2
+// cache after the first time, at a cost that grows with the rows; the tile kernel's is that
+// of 128, and over the cache that of converting every code to 16 bits.  Us of the two,
+// d = 128, few rows / tiles:
+//                                  8 rows       16 rows      32 rows      64 rows
+//   bf16   32,768 keys, 64 heads   166 / 165    281 / 166    541 / 166
+//           2,048 keys, 160 heads   38 / 48      57 / 49      98 / 51
+//           2,048 keys, 8 heads    9.0 / 10.0   9.2 / 10.0   11.6 / 10.2  17.0 / 11.1
+//             320 keys, 2 heads    5.7 / 8.3    5.8 / 8.4    5.9 / 8.4    5.9 / 8.3
+//   8 bits 32,768 keys, 64 heads    97 / 300    171 / 300    319 / 319    599 / 306
+//           2,048 keys, 160 heads   22 / 74      38 / 75      75 / 78     125 / 82
+//             320 keys, 2 heads    6.8 / 9.6    6.8 / 9.4    6.7 / 9.7    6.8 / 10.0
+bool few_rows(const WinArgs &a) {
+    const int64_t rows = (int64_t)a.G * a.Lq;
+    return rows <= (a.k8 ? 32 : 8) || (rows <= 64 && window_tiles(a.w, a.Lq, a.Lq, a.Lk, 16) <= 32);
+}
 int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);

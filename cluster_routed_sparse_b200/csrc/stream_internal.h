@@ -92,7 +92,7 @@ struct WinArgs {
 };
 int64_t window_mma_workspace(const WinArgs &a);   // any number of rows
 cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s);
-int64_t window_few_workspace(const WinArgs &a);   // G * Lq <= 8 rows, 16 over the cache
+int64_t window_few_workspace(const WinArgs &a);   // a few times 8 rows for each key head
 cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s);
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s);
 

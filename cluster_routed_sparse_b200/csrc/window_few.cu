@@ -1,15 +1,13 @@
 // window_few.cu -- the same attention for few query rows: single tokens, or a few,
-// with G * Lq <= 8 rows for each key head over bf16 keys, <= 16 over the 8-bit cache.
+// with 8 rows (G heads x tokens) of a key head to a CTA, over bf16 keys or the 8-bit cache.
 //
-// Bound by reading K and V once.  A warp takes 16 keys at a time, and the rows are
+// Bound by reading K and V once.  A warp takes 16 keys at a time, and its 8 rows are
 // the short side of m16n8k16 products: S^T = K Q^T, the running softmax of
 // window_attn.cu, O^T += V^T P^T, with P^T transposed in registers.  K and V go from
 // global memory straight into the products' operand registers: the order of the
 // contraction over d, and of the output rows, is free, so each thread owns d / 4
 // consecutive elements of two key rows and d / 8 of four value rows, loads them
-// 16 bytes at a time, and the rows of a warp are read whole.  The tile kernel would
-// spend its time on the 112 or more empty rows of its products; here the products are
-// a small part of the issue slots.
+// 16 bytes at a time, and the rows of a warp are read whole.
 //
 // The next K rows are loaded as soon as the products of the present ones have
 // taken theirs, and the same for V: every warp has one of the two in flight.
@@ -19,9 +17,9 @@
 // One token of four sequences over 16,384 of 32,760 bf16 keys and 128 first ones, 40
 // heads (1.35 GB): 209 us in a graph, the rate of a copy.  One token of eight sequences
 // over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 93 us, 5.8 TB/s, 90% of it;
-// the rest is the joining launch and the last wave.  With 9 to 16 rows the registers
-// leave three CTAs on an SM and the loads in flight no longer cover their latency: 188
-// us over that cache.
+// the rest is the joining launch and the last wave.  More rows take as many CTAs, which
+// find the keys in the L2 cache: 171 us for 16 rows over that cache (in one CTA: 183, the
+// registers then leave three of them on an SM), 319 for 32.
 //
 // Types, scales and roundings as in the tile kernel: bf16 over bf16 keys, fp16 with
 // the scales in the exponents over the 8-bit cache.
@@ -51,7 +49,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 struct FewParams {
     WinArgs a;
-    int nsplit;
+    int nsplit, groups;
     float scale_log2;
     float *part_o, *part_lse;
 };
@@ -73,30 +71,31 @@ __device__ __forceinline__ void load_bytes(uint32_t (&r)[BYTES / 4], const void 
     }
 }
 
-// RT: tiles of 8 rows (1, or 2 over the cache).  One tile takes few enough registers for another CTA
-// on the SM, hence more loads in flight.
-template <int D, bool C8, int RT>
-__global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(const __grid_constant__ FewParams fp) {
+// The CTAs of the 8-row groups of a key head stand side by side.
+template <int D, bool C8>
+__global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __grid_constant__ FewParams fp) {
     const WinArgs &p = fp.a;
     constexpr int ES = C8 ? 1 : 2;        // bytes of a stored element
     constexpr int KB = D / 4 * ES;        // bytes of a key row that a thread owns
     constexpr int VB = D / 8 * ES;        // of a value row
     constexpr int KS = D / 16;            // k16 steps of S
     constexpr int DT = D / 16;            // m16 tiles of O^T
-    constexpr int NR = 2 * RT;            // rows of a thread
+    constexpr int NR = 2;                 // rows of a thread
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
 
     release_successor();
     int idx = blockIdx.x;
+    const int row0 = idx % fp.groups * 8;  // the CTA's first row: token row / G, head row % G
+    idx /= fp.groups;
     const int sp = idx % fp.nsplit;
     idx /= fp.nsplit;
     const int hk = idx % p.Hk, b = idx / p.Hk;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
-    const int off = kl - ql, rows = p.G * p.Lq;
+    const int off = kl - ql, rows = p.G * p.Lq - row0;
     int lo_c = 0, hi_c = 0;
-    if (ql > 0) {
-        lo_c = row_range(p.w, off, kl).lo;
-        hi_c = row_range(p.w, ql - 1 + off, kl).hi;
+    if (row0 / p.G < ql) {
+        lo_c = row_range(p.w, row0 / p.G + off, kl).lo;
+        hi_c = row_range(p.w, min((row0 + 7) / p.G, ql - 1) + off, kl).hi;
     }
     const int sink_c = min(p.w.sinks, hi_c);
     const int w0 = lo_c / kChunk, w1 = (hi_c + kChunk - 1) / kChunk;
@@ -105,18 +104,16 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
     const int j0 = (int)((long long)n_all * sp / fp.nsplit), j1 = (int)((long long)n_all * (sp + 1) / fp.nsplit);
     auto chunk_base = [&](int j) { return (j < nsink ? j : w0 + (j - nsink)) * kChunk; };
 
-    // ---- Q^T as the B operand: k16 step s holds elements t4 D/4 + 4 s + {0..3} of row 8 rt + g8
-    uint32_t bq[RT][KS][2];
-    float g_c[RT];  // scale log2(e), times the power of two taken out of that row
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = g8 + 8 * rt;
+    // ---- Q^T as the B operand: k16 step s holds elements t4 D/4 + 4 s + {0..3} of row g8
+    uint32_t bq[KS][2];
+    float g_c = fp.scale_log2;  // scale log2(e), times the power of two taken out of that row
+    {
         uint32_t w[D / 8];
-        const bool live = r < rows && r / p.G < ql;
+        const int i = (row0 + g8) / p.G, g = (row0 + g8) % p.G;
+        const bool live = g8 < rows && i < ql;
         const bf16 *src = static_cast<const bf16 *>(p.q.p);
-        if (live) src += b * p.q.b + (int64_t)(hk * p.G + r % p.G) * p.q.h + (int64_t)(r / p.G) * p.q.l + t4 * (D / 4);
+        if (live) src += b * p.q.b + (int64_t)(hk * p.G + g) * p.q.h + (int64_t)i * p.q.l + t4 * (D / 4);
         load_bytes<D / 2>(w, src, live);
-        g_c[rt] = fp.scale_log2;
         if constexpr (C8) {
             uint32_t top = 0;
 #pragma unroll
@@ -124,26 +121,26 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             const int ex = top ? min(max((int)(top >> 7) - 127, -120), 120) : 0;  // |q| < 2^(ex + 1)
-            g_c[rt] *= exp2i(ex);
+            g_c *= exp2i(ex);
             const float dn = exp2i(-ex);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
         }
 #pragma unroll
-        for (int s = 0; s < KS; ++s) bq[rt][s][0] = w[2 * s], bq[rt][s][1] = w[2 * s + 1];
+        for (int s = 0; s < KS; ++s) bq[s][0] = w[2 * s], bq[s][1] = w[2 * s + 1];
     }
-    // ---- this thread's rows of the scores: e = 2 rt + x is row 8 rt + 2 t4 + x
+    // ---- this thread's rows of the scores: e is row 2 t4 + e
     RowRange rr[NR];
     int sink[NR];
     float row_c[NR];
 #pragma unroll
     for (int e = 0; e < NR; ++e) {
-        const int r = 8 * (e >> 1) + 2 * t4 + (e & 1), i = r / p.G;
+        const int r = 2 * t4 + e, i = (row0 + r) / p.G;
         rr[e] = RowRange{0, 0x7FFFFFFF};  // a row that does not exist never asks for a mask
         if (r < rows && i < ql) rr[e] = row_range(p.w, i + off, kl);
         else if (r < rows) rr[e] = RowRange{0, 0};
         sink[e] = min(p.w.sinks, rr[e].hi);
-        row_c[e] = __shfl_sync(0xFFFFFFFFu, g_c[e >> 1], 4 * (2 * t4 + (e & 1)));
+        row_c[e] = __shfl_sync(0xFFFFFFFFu, g_c, 4 * (2 * t4 + e));
     }
 
     // ---- addresses of a chunk's rows.  The table entry is loaded one chunk ahead.
@@ -185,13 +182,11 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
         }
     };
 
-    float acc[RT][DT][4];
+    float acc[DT][4];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int n = 0; n < DT; ++n)
 #pragma unroll
-        for (int n = 0; n < DT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[rt][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
     float m[NR], l[NR];
 #pragma unroll
     for (int e = 0; e < NR; ++e) m[e] = -INFINITY, l[e] = 0.f;
@@ -212,12 +207,8 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
         if (more) nxt = rows_of(base2, entry, ks_next, vs_next);
         entry = entry_of(j + 2 * kWarps);
 
-        // S^T: s[rt][2 u + x] is key g8 + 8 u, row 8 rt + 2 t4 + x
-        float s[RT][4];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[rt][e] = 0.f;
+        // S^T: s[2 u + e] is key g8 + 8 u, row 2 t4 + e
+        float s[4] = {};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             uint32_t a[4];
@@ -230,8 +221,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
                     a[u] = kw[u][2 * k], a[2 + u] = kw[u][2 * k + 1];
                 }
             }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) mma<C8>(s[rt], a[0], a[1], a[2], a[3], bq[rt][k][0], bq[rt][k][1]);
+            mma<C8>(s, a[0], a[1], a[2], a[3], bq[k][0], bq[k][1]);
         }
         if (more) load_k(nxt, base2);
 
@@ -241,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
         for (int e = 0; e < NR; ++e) {
             full = full && base + kChunk <= rr[e].hi && (base >= rr[e].lo || base + kChunk <= sink[e]);
             const float c = C8 ? row_c[e] * ks : row_c[e];
-            s[e >> 1][e & 1] *= c, s[e >> 1][2 + (e & 1)] *= c;
+            s[e] *= c, s[2 + e] *= c;
         }
         if (!full) {
 #pragma unroll
@@ -249,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int key = base + g8 + 8 * u;
-                    float &x = s[e >> 1][2 * u + (e & 1)];
+                    float &x = s[2 * u + e];
                     x = key < rr[e].hi && (key >= rr[e].lo || key < sink[e]) ? x : -INFINITY;
                 }
         }
@@ -258,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
         bool grows = false;
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
-            top[e] = ev + fmaxf(s[e >> 1][e & 1], s[e >> 1][2 + (e & 1)]);
+            top[e] = ev + fmaxf(s[e], s[2 + e]);
             grows = grows || top[e] > m[e] + 8.f;
         }
         // The maximum moves when some row's grew by more than 2^8 (or is the first).
@@ -273,26 +263,22 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
                 m[e] = mn;
                 l[e] *= al;
 #pragma unroll
-                for (int n = 0; n < DT; ++n) acc[e >> 1][n][e & 1] *= al, acc[e >> 1][n][2 + (e & 1)] *= al;
+                for (int n = 0; n < DT; ++n) acc[n][e] *= al, acc[n][2 + e] *= al;
             }
         }
-        // weights, and P^T as the B operand: keys 8 u + 2 t4 + {0, 1} of row 8 rt + g8
+        // weights, and P^T as the B operand: keys 8 u + 2 t4 + {0, 1} of row g8
         const float inv_vs = C8 ? ex2_approx(-ev) : 1.f;
-        uint32_t bp[RT][2];
+        uint32_t bp[2];
+        float pr[2][2];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float pr[2][2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int e = 2 * rt + x;
-                const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
-                pr[0][x] = ex2_approx(s[rt][x] - mu), pr[1][x] = ex2_approx(s[rt][2 + x] - mu);
-                const float sum = pr[0][x] + pr[1][x];
-                l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) bp[rt][u] = transpose8x8(C8 ? pack_half2(pr[u][0], pr[u][1]) : pack_bf16x2(pr[u][0], pr[u][1]));
+        for (int e = 0; e < NR; ++e) {
+            const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
+            pr[0][e] = ex2_approx(s[e] - mu), pr[1][e] = ex2_approx(s[2 + e] - mu);
+            const float sum = pr[0][e] + pr[1][e];
+            l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) bp[u] = transpose8x8(C8 ? pack_half2(pr[u][0], pr[u][1]) : pack_bf16x2(pr[u][0], pr[u][1]));
         // O^T: row g8 of m16 tile n is element g8 D/8 + 2 n, row g8 + 8 the next one.  (Values in a
         // page with a scale below 2^-90 count as zeros.)
         if (!C8 || vs >= kMinScale) {
@@ -309,8 +295,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
                     a[0] = __byte_perm(vw[0][n], vw[1][n], 0x5410), a[1] = __byte_perm(vw[0][n], vw[1][n], 0x7632);
                     a[2] = __byte_perm(vw[2][n], vw[3][n], 0x5410), a[3] = __byte_perm(vw[2][n], vw[3][n], 0x7632);
                 }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) mma<C8>(acc[rt][n], a[0], a[1], a[2], a[3], bp[rt][0], bp[rt][1]);
+                mma<C8>(acc[n], a[0], a[1], a[2], a[3], bp[0], bp[1]);
             }
         }
         if (more) load_v(nxt, base2);
@@ -318,21 +303,21 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
     }
 
     // ---- join the four warps
-    __shared__ float s_m[kWarps][8 * RT], s_l[kWarps][8 * RT];
-    __shared__ __align__(16) float s_o[kWarps][8 * RT][D + 4];
+    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+    __shared__ __align__(16) float s_o[kWarps][8][D + 4];
 #pragma unroll
     for (int e = 0; e < NR; ++e) {
-        const int r = 8 * (e >> 1) + 2 * t4 + (e & 1);
+        const int r = 2 * t4 + e;
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], o);
         if (g8 == 0) s_m[warp][r] = m[e], s_l[warp][r] = l[e];
 #pragma unroll
         for (int n = 0; n < DT; ++n)
             *reinterpret_cast<float2 *>(&s_o[warp][r][g8 * (D / 8) + 2 * n]) =
-                make_float2(acc[e >> 1][n][e & 1], acc[e >> 1][n][2 + (e & 1)]);
+                make_float2(acc[n][e], acc[n][2 + e]);
     }
     __syncthreads();
-    constexpr int TPR = kThreads / (8 * RT); // threads of a row
+    constexpr int TPR = kThreads / 8;       // threads of a row
     constexpr int EPT = D / TPR;            // elements of a thread
     const int r = tid / TPR, e0 = (tid % TPR) * EPT;
     if (r >= rows) return;
@@ -344,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
         wgt[w] = s_m[w][r] == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - top);
         sum += wgt[w] * s_l[w][r];
     }
-    const int i = r / p.G, h = hk * p.G + r % p.G;
+    const int i = (row0 + r) / p.G, h = hk * p.G + (row0 + r) % p.G;
     const bool some = i < ql && sum > 0.f;
     const float inv = some ? 1.f / sum : 0.f;
     const float lse = some ? (top + __log2f(sum)) * 0.693147180559945f : -INFINITY;
@@ -371,13 +356,15 @@ __global__ void __launch_bounds__(kThreads, (C8 ? 5 : 4) - RT) k_window_few(cons
     }
 }
 
+int few_groups(const WinArgs &a) { return (int)(((int64_t)a.G * a.Lq + 7) / 8); }
+
 // Parts of the keys: as many as make the waves of CTAs come out full, a CTA costing
 // its 16-key chunks and about ten more for its start and end, no part below 256 keys.
 // (32,760 cached tokens, 64 key heads in all: 180, 109, 111, 114 and 125 us with 4, 9,
 // 18, 27 and 37 parts.)
 int few_split(const WinArgs &a) {
-    const int64_t n = window_tiles(a.w, a.Lq, a.Lq, a.Lk, kChunk), units = (int64_t)a.B * a.Hk;
-    const int64_t slots = 148 * ((a.k8 ? 5 : 4) - ((int64_t)a.G * a.Lq <= 8 ? 1 : 2));
+    const int64_t n = window_tiles(a.w, a.Lq, a.Lq, a.Lk, kChunk), units = (int64_t)a.B * a.Hk * few_groups(a);
+    const int64_t slots = 148 * (a.k8 ? 4 : 3);
     int64_t best = INT64_MAX;
     int parts = 1;
     for (int64_t waves = 0; waves <= 8; ++waves) {
@@ -398,23 +385,17 @@ int64_t window_few_workspace(const WinArgs &a) {
 cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s) {
     FewParams p{};
     p.a = a;
-    p.nsplit = few_split(a);
+    p.nsplit = few_split(a), p.groups = few_groups(a);
     p.scale_log2 = a.scale * 1.44269504088896f;
     if (p.nsplit > 1) {
         p.part_o = static_cast<float *>(a.ws);
         p.part_lse = p.part_o + (int64_t)p.nsplit * a.B * a.Hq * a.Lq * a.d;
     }
-    const int64_t grid = (int64_t)a.B * a.Hk * p.nsplit;
+    const int64_t grid = (int64_t)a.B * a.Hk * p.nsplit * p.groups;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     auto go = [&](auto kern) { kern<<<(unsigned)grid, kThreads, 0, s>>>(p); };
-    const bool half = (int64_t)a.G * a.Lq <= 8;
-    if (a.d == 128) {
-        if (a.k8) half ? go(k_window_few<128, true, 1>) : go(k_window_few<128, true, 2>);
-        else go(k_window_few<128, false, 1>);
-    } else {
-        if (a.k8) half ? go(k_window_few<64, true, 1>) : go(k_window_few<64, true, 2>);
-        else go(k_window_few<64, false, 1>);
-    }
+    if (a.d == 128) a.k8 ? go(k_window_few<128, true>) : go(k_window_few<128, false>);
+    else a.k8 ? go(k_window_few<64, true>) : go(k_window_few<64, false>);
     AC_NOTE_LAUNCH();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.nsplit == 1) return e;
