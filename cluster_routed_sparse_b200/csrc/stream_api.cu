@@ -53,8 +53,40 @@ bool few_rows(const WinArgs &a) {
     const int64_t rows = (int64_t)a.G * a.Lq;
     return rows <= (a.k8 ? 32 : 8) || (rows <= 64 && window_tiles(a.w, a.Lq, a.Lq, a.Lk, 16) <= 32);
 }
-int64_t window_workspace(const WinArgs &a) { return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a); }
+// Many rows over the cache: its visible part is written out as bf16 once, instead of
+// being converted by every CTA for its 256 rows.  Us of the two, d = 128, codes / bf16:
+//                            512 rows    1,024       1,560       3,120
+//    16,384 keys, 12 heads    76 / 84    133 / 123   242 / 207   447 / 331
+//     8,192 keys, 32 heads   113 / 113   189 / 157   355 / 265   515 / 366
+//     2,048 keys, 8 heads     23 / 24     30 / 30     43 / 38     52 / 42
+//       512 keys, 2 heads     13 / 14     13 / 14     13 / 15     15 / 17   (d = 64)
+// A call that would need more than 1 GiB for it (262,144 tokens of 8 heads) reads the codes.
+constexpr int64_t kExpandRows = 768, kExpandKeys = 16384, kExpandMost = int64_t(1) << 30;
+int64_t expand_bytes(const WinArgs &a) { return (int64_t)a.B * a.Hk * a.Lk * a.d * 4; }
+bool expands(const WinArgs &a) {
+    return a.k8 && !few_rows(a) && (int64_t)a.G * a.Lq > kExpandRows && (int64_t)a.B * a.Hk * a.Lk >= kExpandKeys &&
+           expand_bytes(a) <= kExpandMost;
+}
+// The call over the rows written out, which stand in front of its own workspace.
+WinArgs expanded(const WinArgs &a) {
+    WinArgs x = a;
+    const int64_t n = (int64_t)a.Hk * a.Lk * a.d, half = expand_bytes(a) / 2;
+    x.k = View{a.ws, n, (int64_t)a.Lk * a.d, a.d};
+    x.v = View{static_cast<char *>(a.ws) + half, n, (int64_t)a.Lk * a.d, a.d};
+    x.ws = static_cast<char *>(a.ws) + 2 * half;
+    x.k8 = x.v8 = nullptr;
+    return x;
+}
+int64_t window_workspace(const WinArgs &a) {
+    if (expands(a)) return expand_bytes(a) + window_mma_workspace(expanded(a));
+    return few_rows(a) ? window_few_workspace(a) : window_mma_workspace(a);
+}
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
+    if (expands(a)) {
+        const WinArgs x = expanded(a);
+        const cudaError_t e = launch_cache8_expand(a, static_cast<bf16 *>(x.k.p), static_cast<bf16 *>(x.v.p), s);
+        return e == cudaSuccess ? launch_window_mma(x, s) : e;
+    }
     return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);
 }
 

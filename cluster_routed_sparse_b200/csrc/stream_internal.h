@@ -96,6 +96,8 @@ int64_t window_few_workspace(const WinArgs &a);   // a few times 8 rows for each
 cudaError_t launch_window_few(const WinArgs &a, cudaStream_t s);
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const WinArgs &a, int nsplit, cudaStream_t s);
 
+cudaError_t launch_cache8_expand(const WinArgs &a, __nv_bfloat16 *k, __nv_bfloat16 *v, cudaStream_t s);
+
 struct WinBwdArgs {
     WinArgs f;                  // q, k, v, o, lse as the forward left them
     View go, dq, dk, dv;

@@ -520,7 +520,9 @@ AC_API ac_status ac_cache8_append(const ac_cache8 *cache, const ac_view *k, cons
  * [B]) the tokens in the cache.  Pages that no query sees are not read, their
  * table entries may be anything; a visible page whose index is out of range
  * reads as zeros (AC_ERR_BOUNDS).  Values in pages with a scale below 2^-90
- * count as zeros.  The NaN codes of a cache behind its sequences do no harm. */
+ * count as zeros.  The NaN codes of a cache behind its sequences do no harm.  With
+ * many query rows the workspace holds the visible keys and values in 16 bits too
+ * (max_pages page_tokens tokens of every sequence, where that is at most 1 GiB). */
 AC_API ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B, int32_t Hq, int32_t Lq,
                                           int32_t max_pages, const ac_window *w, int64_t *bytes);
 AC_API ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, const ac_view *o, float *lse, int32_t B,

@@ -452,6 +452,53 @@ def test_cache8_attn(case, T):
     ref.check("lse", lse, r)
 
 
+@pytest.mark.parametrize("T", [16, 64, 128])
+@pytest.mark.parametrize("case", [
+    (2, 4, 2, 500, 4200, 128, 900, 0, 100, 1),
+    (1, 8, 8, 800, 2100, 64, 1, 0, 250, 300),
+    (1, 2, 1, 700, 17000, 128, 300, 20, 0, 1),
+    (3, 6, 3, 450, 1900, 128, -1, -1, 0, 1),
+])
+def test_cache8_attn_of_many_rows(case, T):
+    """More rows than a few tiles: ragged sequences, NaN codes behind them, junk in the table wherever
+    no query sees the page, and one page that is visible and bad, which reads as zeros."""
+    B, Hq, Hk, Lq, Lk, d = case[:6]
+    g = gen(2 * T + Lk)
+    per = (Lk + T - 1) // T
+    c = random_cache(g, B * per + 1, Hk, T, d)
+    table = torch.randperm(B * per, generator=g, device="cuda").view(B, per).to(torch.int32)
+    lens = torch.tensor([max(1, Lk - 77 * b) for b in range(B)], device="cuda", dtype=torch.int32)
+    q_lens = torch.tensor([Lq - 40 * b for b in range(B)], device="cuda", dtype=torch.int32)
+    for b in range(B):
+        n = int(lens[b])
+        last = int(table[b, (n - 1) // T])
+        if n % T:
+            c.k.view(torch.uint8)[last, :, n % T:] = 0x7F
+            c.v.view(torch.uint8)[last, :, n % T:] = 0xFF
+    k, v = dense(c, table, Lk)
+    mask = ref.visible(B, Lq, Lk, *case[6:], q_lens, lens)
+    seen = mask.reshape(B, -1, mask.shape[-2], Lk).any(2).any(1)  # [B, Lk]
+    pages = torch.nn.functional.pad(seen, (0, per * T - Lk)).view(B, per, T).any(2)
+    table = torch.where(pages, table, -9)
+    bad = int(pages[0].nonzero()[-2])
+    keep = (torch.arange(Lk, device="cuda") < lens.view(B, 1)).view(B, 1, Lk, 1)
+    q = normal(g, B, Hq, Lq, d)
+    for broken in (False, True):
+        if broken:
+            table[0, bad] = B * per + 1
+            keep = keep.clone()
+            keep[0, :, bad * T:(bad + 1) * T] = False
+        out = torch.full_like(q, math.nan)
+        o, lse = crs.cache8_attn(q, c, table, lens, q_lens=q_lens, return_lse=True, out=out, **rule(case))
+        if broken:
+            with pytest.raises(Exception, match="out of range"):
+                crs.ops_status()
+        crs.ops_status()
+        r = ref.attention(q, torch.where(keep, k, 0.0), torch.where(keep, v, 0.0), mask)
+        ref.check("o", o, r)
+        ref.check("lse", lse, r)
+
+
 @pytest.mark.parametrize("Lq", [1, 40])
 def test_cache8_attn_scales_of_very_different_size(Lq):
     """Pages of zeros (the smallest scale), pages 2^40 apart, and queries of any size."""
