@@ -2,6 +2,7 @@
 // argument blocks and the error words.
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 
 #include "stream_device.cuh"
 
@@ -90,6 +91,28 @@ cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);
 }
 
+// Turns per step modulo 1 of n frequencies, in units of 2^-64, to the nearest.  The last
+// frequencies' stay at hand: 0.5 us of a call of 8 us.
+bool turns_of(const double *freq, int n, uint64_t *turns) {
+    thread_local double last[128];
+    thread_local uint64_t last_turns[128];
+    thread_local int last_n = -1;
+    if (n != last_n || memcmp(freq, last, n * sizeof(double))) {
+        last_n = -1;
+        for (int k = 0; k < n; ++k) {
+            if (!std::isfinite(freq[k])) return false;
+            long double t = (long double)freq[k] * 0.159154943091895335768883763372514362L;
+            if (t >= 1.0L || t <= -1.0L) t = fmodl(t, 1.0L);
+            const uint64_t units = (uint64_t)((t < 0 ? -t : t) * 18446744073709551615.0L + 0.5L);
+            last_turns[k] = t < 0 ? 0 - units : units;
+            last[k] = freq[k];
+        }
+        last_n = n;
+    }
+    memcpy(turns, last_turns, n * sizeof(uint64_t));
+    return true;
+}
+
 View view_of(const ac_view *v) { return View{v->data, v->stride_b, v->stride_h, v->stride_l}; }
 
 // 16-byte rows: what the vector and bulk tensor loads need.  A stride of a
@@ -175,18 +198,9 @@ extern "C" ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view
     a.P = 0;
     for (int i = 0; i < n_axes; ++i) {
         if (pairs[i] < 0 || pairs[i] > d / 2 - a.P) return refuse("ac_rope_axes: the axes' pairs must fit in d / 2");
-        for (int k = 0; k < pairs[i]; ++k) {
-            const double f = freq[a.P];
-            if (!std::isfinite(f)) return refuse("ac_rope_axes: frequencies must be finite");
-            // turns per step modulo 1, in units of 2^-64, to the nearest
-            long double t = (long double)f * 0.159154943091895335768883763372514362L;
-            if (t >= 1.0L || t <= -1.0L) t = fmodl(t, 1.0L);
-            const uint64_t units = (uint64_t)((t < 0 ? -t : t) * 18446744073709551615.0L + 0.5L);
-            a.turns[a.P] = t < 0 ? 0 - units : units;
-            a.axis[a.P] = (uint8_t)i;
-            ++a.P;
-        }
+        for (int k = 0; k < pairs[i]; ++k) a.axis[a.P++] = (uint8_t)i;
     }
+    if (!turns_of(freq, a.P, a.turns)) return refuse("ac_rope_axes: frequencies must be finite");
     if (B == 0 || L == 0 || H + H2 == 0) return AC_OK;
     if (!positions || (H && (!x || !y || !x->data || !y->data)) || (H2 && (!x2 || !y2 || !x2->data || !y2->data)))
         return refuse("ac_rope_axes: NULL tensor");

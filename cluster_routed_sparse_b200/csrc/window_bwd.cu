@@ -631,13 +631,14 @@ __global__ void __launch_bounds__(256) k_sum_parts(const BwdParams p) {
     const int b = bh / p.Hk, hk = bh % p.Hk, r0 = tile * 128;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
     const int parts = key_tile(p, r0, ql, kl).parts;
+    wait_predecessor();  // (always: the end of this kernel stands for the end of the one before)
     if (parts == 1) return;
-    wait_predecessor();
     const float4 *src = reinterpret_cast<const float4 *>(p.parts + ((int64_t)bh * p.part_tiles + tile) * p.max_parts * 2 * 128 * D);
     for (int t = blockIdx.y * 256 + threadIdx.x; t < 2 * 128 * D / 4; t += gridDim.y * 256) {
         const int half = t / (128 * D / 4), row = t / (D / 4) % 128, e = t % (D / 4) * 4;
         if (r0 + row >= p.Lk) continue;
         float4 s = src[t];
+#pragma unroll 4
         for (int i = 1; i < parts; ++i) {
             const float4 x = src[(int64_t)i * (2 * 128 * D / 4) + t];
             s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
