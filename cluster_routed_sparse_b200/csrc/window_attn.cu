@@ -14,7 +14,8 @@
 // where some row of the warp does not see all of them.
 //
 // Warp roles (three warpgroups; five over 8-bit keys):
-//   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t
+//   warps 0-3 / 4-7  softmax + epilogue of row tile 0 / 1; thread t owns row t (bf16 keys, one
+//                    row tile: of its even / odd key tiles)
 //   warp 8           TMA producer (Q; bf16 keys: K and V, and in the last tile it
 //                    zeroes the V rows behind the sequence: 0 x garbage would be NaN)
 //   warp 9           TMEM allocator and tcgen05.mma issuer
@@ -44,13 +45,16 @@
 // Bound by the softmax's chain: a pair of row tiles takes 3,500 cycles per key tile (S
 // 1,100 waited for, its load 150, maximum 320, exponentials 1,310, P 285, per row tile)
 // where the products take 2,048.  Frame-causal, 32,760 tokens in frames of 1,560, three
-// frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,070 us alone, 1.09 PFLOP/s, 65%
-// of the measured cuBLAS rate; 1,220 us in a long loop under the power limit.  A frame
-// of 1,560 over 18,720 cached tokens, 12 heads (0.18 TFLOP): 295 us, 36%; every CTA
-// converts the codes anew.  Dropped, in us of these two workloads: two threads a row
-// (1,266 in the loop; 595), a quarter of the exponentials as a polynomial on the FMA pipe
-// (no difference), a persistent CTA (1,059 against 1,028; 440 against 349 then), S in
-// 64-key halves that go round on their own (1,215 in the loop; 341).
+// frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,030 us alone, 1.13 PFLOP/s, 67%
+// of the measured cuBLAS rate; 1,190 us in a long loop under the power limit.  1,560
+// rows over 18,720 keys, 12 heads (0.18 TFLOP): 204 us; over the codes of the 8-bit cache
+// 295, because every CTA converts them anew and reads its scores twice (registers go to
+// the converting threads): many rows take the cache as bf16 rows instead.  Dropped, in us
+// of the two workloads (codes): two threads a row (1,266 in the loop; 595), a quarter of the
+// exponentials as a polynomial on the FMA pipe (no difference), a persistent CTA (1,059
+// against 1,028; 440 against 349 then), S in 64-key halves that go round on their own
+// (1,215 in the loop; 341), each converting register refilled as soon as it is free (17 rows:
+// 258 -> 290).
 //
 // Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
 // issued and frees its TMEM.
@@ -802,9 +806,10 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const
 
 // Parts of the key tiles.  A CTA takes about (tiles + 4) tile times (its start
 // and end cost as much as four), 148 run at once, and joining reads and writes
-// the partial O; a tile time is about 1.9 us, 2.6 us over the cache (a frame of 1,560
-// tokens over 18,720 cached ones: 429, 326, 360, 309 and 314 us with 2, 3, 4, 5 and 7
-// parts).
+// the partial O; a tile time is about 1.9 us, 2.6 us over the cache's codes.  (Us with 1, 2,
+// 3, 5, 8 and 14 parts: 1,560 rows of 12 heads over 18,720 keys 261, 227, 204, 199, 228,
+// 261; 300 rows of 8 heads over 8,192 keys 118, 68, 52, 38, 30, 37; 1,560 rows of 40
+// heads over those 241, 302, 323, 353, 409, 539.)
 struct Plan {
     int TT, tiles_q, nsplit;
 };
