@@ -44,7 +44,8 @@
 // exponentials 1,024, dS 670, and in the second role the statistics 420).  Short loops
 // (clips) pay for their start: 4,800 cycles until the first tiles are there, a tile and
 // a half.  Dropped: P and dS in column halves of 64 that go round on their own (5,264
-// us with the forward, against 5,100); a barrier for each fixed tile (no difference).
+// us with the forward, against 5,100); a barrier for each fixed tile, and
+// an eighth to a third of the exponentials as a quartic on the FMA pipe (no difference).
 #include "stream_device.cuh"
 #include "stream_host.h"
 
@@ -139,44 +140,49 @@ __device__ __forceinline__ KeyTile key_tile(const BwdParams &p, int r0, int ql, 
 
 // -lse log2(e) (-inf for a row without keys, so that its P is 0) and
 // delta0 = sum dO o of every row of the query tiles, in the order of the tiles.
-// D / 8 lanes per row; bound by reading dO and o once.
+// A CTA takes a query tile, D / 8 lanes a row; bound by reading dO and o once (9,360
+// tokens of 12 heads, d = 128, 57 MB: 15 us).
 template <int D>
 __global__ void __launch_bounds__(256) k_row_stats(View go, View o, const float *__restrict__ lse, BwdParams p) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 8, RPP = 256 / LPR, N = 4;  // lanes of a row, rows of a pass, passes with loads in flight
     release_successor();
-    const int64_t idx = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-    const int part = threadIdx.x % LPR;
-    const int row = (int)(idx % 128);
-    const int64_t tile = idx / 128;
-    const int qt = (int)(tile % p.tiles_q);
-    const int64_t bh = tile / p.tiles_q;
-    if (bh >= (int64_t)p.B * p.Hk) return;  // whole warps: 128 rows of a tile
-    const int b = (int)(bh / p.Hk), hk = (int)(bh % p.Hk);
-    const int i = qt * p.TT + row / p.G, h = hk * p.G + row % p.G;
+    const int qt = blockIdx.x % (unsigned)p.tiles_q, bh = blockIdx.x / (unsigned)p.tiles_q;
+    const int b = bh / p.Hk, hk = bh % p.Hk;
+    const int part = threadIdx.x % LPR, first = threadIdx.x / LPR;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err);
-    const bool live = row < p.G * p.TT && i < ql;
-    float s = 0.f;
-    if (live) {
-        const uint4 x = *(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(go.p) + b * go.b + h * go.h + i * go.l) + part);
-        const uint4 y = *(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(o.p) + b * o.b + h * o.h + i * o.l) + part);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const bf16 *gb = static_cast<const bf16 *>(go.p) + b * go.b + hk * p.G * go.h, *ob = static_cast<const bf16 *>(o.p) + b * o.b + hk * p.G * o.h;
+    const float *lb = lse + ((int64_t)b * p.Hq + hk * p.G) * p.Lq;
+    float *st = p.stats + ((int64_t)bh * p.tiles_q + qt) * kStats;
+    for (int r0 = first; r0 < 128; r0 += N * RPP) {
+        uint4 x[N], y[N];
+        float l[N];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-            s = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), s);
+        for (int k = 0; k < N; ++k) {
+            const int row = r0 + k * RPP, i = qt * p.TT + row / p.G, g = row % p.G;
+            x[k] = y[k] = make_uint4(0, 0, 0, 0), l[k] = -INFINITY;
+            if (row < p.G * p.TT && i < ql) {
+                x[k] = *(reinterpret_cast<const uint4 *>(gb + g * go.h + i * go.l) + part);
+                y[k] = *(reinterpret_cast<const uint4 *>(ob + g * o.h + i * o.l) + part);
+                l[k] = lb[(int64_t)g * p.Lq + i];
+            }
         }
-    }
 #pragma unroll
-    for (int m = LPR / 2; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-    if (part == 0) {
-        float nl = -INFINITY;
-        if (live) {
-            const float l = lse[((int64_t)b * p.Hq + h) * p.Lq + i];
-            if (l > -INFINITY) nl = -l * 1.44269504088896f;
+        for (int k = 0; k < N; ++k) {
+            const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+                s = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), s);
+            }
+#pragma unroll
+            for (int m = LPR / 2; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+            if (part == 0) {
+                const int row = r0 + k * RPP;
+                st[row] = l[k] > -INFINITY ? -l[k] * 1.44269504088896f : -INFINITY;
+                st[128 + row] = s;
+            }
         }
-        float *st = p.stats + tile * kStats;
-        st[row] = nl;
-        st[128 + row] = live ? s : 0.f;
     }
 }
 
@@ -704,8 +710,7 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     p.parts = p.stats + stats_floats(a);
     p.chunk = pt.chunk, p.max_parts = pt.max_parts, p.part_tiles = pt.part_tiles;
     const int64_t nq = (int64_t)a.B * a.Hk * p.tiles_q, nk = (int64_t)a.B * a.Hk * p.tiles_k * pt.max_parts;
-    const int64_t stat_blocks = nq * 128 * (a.d / 8) / 256;
-    if (nq > 0x7FFFFFFF || nk > 0x7FFFFFFF || stat_blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (nq > 0x7FFFFFFF || nk > 0x7FFFFFFF) return cudaErrorInvalidValue;
     BwdMaps mq{}, mk{};  // rows = queries; rows = keys
     cudaError_t e = cudaSuccess;
     auto qmap = [&](CUtensorMap *m, const View &v) {
@@ -731,9 +736,9 @@ cudaError_t launch_window_bwd(const WinBwdArgs &g, cudaStream_t s) {
     };
     if (nq > 0) {
         if (a.d == 128)
-            k_row_stats<128><<<(unsigned)stat_blocks, 256, 0, s>>>(g.go, a.o, a.lse, p);
+            k_row_stats<128><<<(unsigned)nq, 256, 0, s>>>(g.go, a.o, a.lse, p);
         else
-            k_row_stats<64><<<(unsigned)stat_blocks, 256, 0, s>>>(g.go, a.o, a.lse, p);
+            k_row_stats<64><<<(unsigned)nq, 256, 0, s>>>(g.go, a.o, a.lse, p);
         AC_NOTE_LAUNCH();
         e = cudaGetLastError();
     }
