@@ -760,20 +760,26 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const
     const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
     if (row >= rows) return;
     wait_predecessor();
+    float mine;  // log-sum-exp of part s0 + lane of the group
+    Vec f[8];    // (loaded whatever they hold, so that all are in flight)
+    auto load = [&](int s0) {
+        const int n = min(8, nsplit - s0);
+        mine = lane < n ? part_lse[(s0 + lane) * rows + row] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const Vec *>(part_o + ((s0 + min(i, n - 1)) * rows + row) * D + lane * N);
+    };
+    if (w0 * 8 < nsplit) load(w0 * 8);
     float top = -INFINITY;
     for (int s = lane; s < nsplit; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
     for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     float acc[N] = {}, sum = 0.f;
     if (top > -INFINITY) {
         for (int s0 = w0 * 8; s0 < nsplit; s0 += WARPS * 8) {
-            const int n = min(8, nsplit - s0);
-            const float mine = lane < n ? __expf(part_lse[(s0 + lane) * rows + row] - top) : 0.f;
-            Vec f[8];  // (loaded whatever it holds, so that all are in flight)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const Vec *>(part_o + ((s0 + min(i, n - 1)) * rows + row) * D + lane * N);
+            if (s0 != w0 * 8) load(s0);
+            const float weight = __expf(mine - top);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float w = __shfl_sync(0xFFFFFFFFu, mine, i);
+                const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
                 const float *x = reinterpret_cast<const float *>(&f[i]);
                 sum += w;
 #pragma unroll
@@ -796,8 +802,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int i = (int)(row % Lq), h = (int)(row / Lq % Hq);
-    const int64_t b = row / Lq / Hq;
+    const uint32_t r = (uint32_t)row, i = r % (uint32_t)Lq, bh = r / (uint32_t)Lq, h = bh % (uint32_t)Hq;  // (at most 2^32 rows)
+    const int64_t b = bh / (uint32_t)Hq;
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<bf16 *>(o.p) + b * o.b + h * o.h + i * o.l) + lane * (N / 2);
 #pragma unroll
     for (int e = 0; e < N; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
