@@ -151,12 +151,15 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // ---- work item: (sequence and key head, pair of row tiles, part of the keys).
-    // Late tiles first: without a left bound they see the most keys.
+    // All heads' late tiles first: they see the most keys (16,384 tokens, causal, 12 heads: 751
+    // -> 652 us).  Without bounds all see the same, and head after head keeps the keys in the L2
+    // cache (1,593 against 1,666 us).
     int idx = blockIdx.x;
     const int sp = idx % p.nsplit;
     idx /= p.nsplit;
-    const int qt = p.tiles_q - 1 - idx % p.tiles_q;
-    const int bh = idx / p.tiles_q;
+    const bool spread = p.w.left >= 0 || p.w.right >= 0;
+    const int bh = spread ? idx % (p.B * p.Hk) : idx / p.tiles_q;
+    const int qt = p.tiles_q - 1 - (spread ? idx / (p.B * p.Hk) : idx % p.tiles_q);
     const int b = bh / p.Hk, hk = bh % p.Hk;
     const int i0 = qt * 2 * p.TT;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);

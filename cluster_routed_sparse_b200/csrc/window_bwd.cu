@@ -197,11 +197,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // ---- work item: (sequence and key head, row tile).  The row tiles with the most
-    // columns first: early keys (first tokens; no left bound), late queries.
+    // columns first, those of all heads: early keys (first tokens; no left bound), late queries
+    // (frames, three and the first: 5,090 -> 4,930 us with the forward; a clip 133 -> 125).  Without
+    // bounds head after head, as in window_attn.cu.
     const int tiles = KEYS ? p.tiles_k : p.tiles_q;
     const int part = KEYS ? blockIdx.x % p.max_parts : 0, item = KEYS ? blockIdx.x / p.max_parts : blockIdx.x;
-    const int bh = item / tiles;
-    const int rt = KEYS ? item % tiles : tiles - 1 - item % tiles;
+    const bool spread = p.w.left >= 0 || p.w.right >= 0;
+    const int bh = spread ? item % (p.B * p.Hk) : item / tiles, nth = spread ? item / (p.B * p.Hk) : item % tiles;
+    const int rt = KEYS ? nth : tiles - 1 - nth;
     const int b = bh / p.Hk, hk = bh % p.Hk;
     const int ql = seq_len(p.q_lens, b, p.Lq, p.err), kl = seq_len(p.k_lens, b, p.Lk, p.err);
     const int off = kl - ql;
