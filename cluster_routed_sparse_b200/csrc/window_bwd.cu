@@ -38,7 +38,7 @@
 // Bound by the tensor core and the hand-offs: 8 products of 128 x 128 x d per tile and
 // role pair, 3 more than one role with atomic sums into dQ would take, which is the
 // price of the same bits every time.  32,760 queries in frames of 1,560 over three
-// frames and the first, 12 heads, d = 128: 4.66 TFLOP in 4.0 ms, 1.16 PFLOP/s, 69% of
+// frames and the first, 12 heads, d = 128: 4.66 TFLOP in 3.8 ms, 1.22 PFLOP/s, 72% of
 // the measured cuBLAS rate; 2,830 cycles a tile in the first role and 3,000 in the
 // second where the products take 2,048 (the scores' wait 500, P 1,380, of which the
 // exponentials 1,024, dS 670, and in the second role the statistics 420).  Short loops
