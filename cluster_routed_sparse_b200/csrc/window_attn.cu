@@ -678,7 +678,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         const bool read = C8 ? active : n_tiles > 0;
-        const bool some = read && live && m_run > -INFINITY;
+        // A row that sees nothing has a sum of exactly 0.  (Its maximum does not tell: the maximum passes over a NaN.)
+        const bool some = read && live && l_run != 0.f;
         const float il = some ? 1.f / l_run : 0.f;
         const int64_t orow = ((int64_t)b * p.Hq + hk * p.G + g) * p.Lq + i;
         if (ok && mine && (pair || wg == 0)) {
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
 }
 
 // Joins the partial results of a row: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  A
-// part that saw nothing has lse_s = -inf and no O_s.  WARPS warps per row, each with the
+// part that saw nothing has lse_s = -inf and no O_s; one with a NaN makes the row NaN.  WARPS warps per row, each with the
 // loads of eight parts in flight; bound by their latency.  (One row of 100,000 keys, 390
 // parts: 101 us in all when one warp read the parts one after the other, 17 now.)
 template <int D, int WARPS>
@@ -773,20 +774,24 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const
     };
     if (w0 * 8 < nsplit) load(w0 * 8);
     float top = -INFINITY;
-    for (int s = lane; s < nsplit; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
+    bool seen = false;
+    for (int s = lane; s < nsplit; s += 32) {
+        const float x = part_lse[s * rows + row];
+        top = fmaxf(top, x), seen = seen || x != -INFINITY;
+    }
     for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     float acc[N] = {}, sum = 0.f;
-    if (top > -INFINITY) {
+    if (__any_sync(0xFFFFFFFFu, seen)) {
         for (int s0 = w0 * 8; s0 < nsplit; s0 += WARPS * 8) {
             if (s0 != w0 * 8) load(s0);
-            const float weight = __expf(mine - top);
+            const float weight = mine == -INFINITY ? -1.f : __expf(mine - top);  // (-1: no O_s)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
                 const float *x = reinterpret_cast<const float *>(&f[i]);
-                sum += w;
+                sum = w < 0.f ? sum : sum + w;
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] = w > 0.f ? fmaf(w, x[e], acc[e]) : acc[e];
+                for (int e = 0; e < N; ++e) acc[e] = w < 0.f ? acc[e] : fmaf(w, x[e], acc[e]);
             }
         }
     }
@@ -804,13 +809,13 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) k_combine(const
             for (int e = 0; e < N; ++e) acc[e] += s_acc[w][lane * N + e];
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const uint32_t r = (uint32_t)row, i = r % (uint32_t)Lq, bh = r / (uint32_t)Lq, h = bh % (uint32_t)Hq;  // (at most 2^32 rows)
     const int64_t b = bh / (uint32_t)Hq;
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<bf16 *>(o.p) + b * o.b + h * o.h + i * o.l) + lane * (N / 2);
 #pragma unroll
     for (int e = 0; e < N; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lse && lane == 0) lse[row] = sum > 0.f ? top + __logf(sum) : -INFINITY;
+    if (lse && lane == 0) lse[row] = sum != 0.f ? top + __logf(sum) : -INFINITY;
 }
 
 // Parts of the key tiles.  A CTA takes about (tiles + 4) tile times (its start

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) k_row_stats(View go, View o, const float 
             for (int m = LPR / 2; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
             if (part == 0) {
                 const int row = r0 + k * RPP;
-                st[row] = l[k] > -INFINITY ? -l[k] * 1.44269504088896f : -INFINITY;
+                st[row] = l[k] == -INFINITY ? -INFINITY : -l[k] * 1.44269504088896f;  // (a NaN stays one)
                 st[128 + row] = s;
             }
         }

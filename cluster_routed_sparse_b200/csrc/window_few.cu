@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
             full = full && base + kChunk <= rr[e].hi && (base >= rr[e].lo || base + kChunk <= sink[e]);
-            const float c = C8 ? row_c[e] * ks : row_c[e];
-            s[e] *= c, s[2 + e] *= c;
+            s[e] *= row_c[e], s[2 + e] *= row_c[e];
+            if (C8) s[e] *= ks, s[2 + e] *= ks;  // (one after the other: the two factors' product may overflow where s is 0)
         }
         if (!full) {
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
         sum += wgt[w] * s_l[w][r];
     }
     const int i = (row0 + r) / p.G, h = hk * p.G + (row0 + r) % p.G;
-    const bool some = i < ql && sum > 0.f;
+    const bool some = i < ql && sum != 0.f;  // a row that sees nothing has a sum of exactly 0; a NaN is no such row
     const float inv = some ? 1.f / sum : 0.f;
     const float lse = some ? (top + __log2f(sum)) * 0.693147180559945f : -INFINITY;
     const int64_t all = (int64_t)p.B * p.Hq * p.Lq, orow = ((int64_t)b * p.Hq + h) * p.Lq + i;

@@ -469,7 +469,8 @@ typedef struct ac_window {
  * q_lens, k_lens: device int32 [B], the lengths of a padded batch (NULL: Lq,
  * Lk).  A row that sees nothing, and a row behind its sequence, gets zeros and
  * lse = -inf; what the keys and values behind k_lens hold does not matter,
- * those before it must be finite.  lse: [B, Hq, Lq] fp32, natural logarithm,
+ * those before it must be finite.  A row with a NaN or an infinity among its
+ * scores (a NaN in the query; products past fp32) is NaN, its lse too.  lse: [B, Hq, Lq] fp32, natural logarithm,
  * nullable.  d 64 or 128, Hq / Hk at most 128, B and Hq at most 65535, Lq and Lk
  * at most 2^30, B Hq Lq and B Hk Lk at most 2^32.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
@@ -482,7 +483,9 @@ AC_API ac_status ac_window_attn(const ac_view *q, const ac_view *k, const ac_vie
 
 /* Its gradients dq, dk, dv from that of o (d_o), with o and lse as the forward
  * left them and the same lengths and window.  Key heads shared by several query
- * heads get the sum.  Rows behind a sequence get zeros.  Bit-identical from run
+ * heads get the sum.  Rows behind a sequence get zeros.  A row that is NaN passes
+ * it to dq and to dk and dv of the keys that it sees, and may to those of keys near
+ * them in its key head.  Bit-identical from run
  * to run (no atomic sums).  Errors as ac_window_attn. */
 AC_API ac_status ac_window_attn_backward_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t Lq, int32_t Lk,
                                                    int32_t d, const ac_window *w, int64_t *bytes);
@@ -520,7 +523,9 @@ AC_API ac_status ac_cache8_append(const ac_cache8 *cache, const ac_view *k, cons
  * [B]) the tokens in the cache.  Pages that no query sees are not read, their
  * table entries may be anything; a visible page whose index is out of range
  * reads as zeros (AC_ERR_BOUNDS).  Values in pages with a scale below 2^-90
- * count as zeros.  The NaN codes of a cache behind its sequences do no harm.  With
+ * count as zeros.  The NaN codes of a cache behind its sequences do no harm; one
+ * within makes the rows that see it NaN (a value that element of theirs, and of rows
+ * near them that do not).  With
  * many query rows the workspace holds the visible keys and values in 16 bits too
  * (max_pages page_tokens tokens of every sequence, where that is at most 1 GiB). */
 AC_API ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B, int32_t Hq, int32_t Lq,
