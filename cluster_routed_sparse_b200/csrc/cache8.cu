@@ -171,7 +171,6 @@ __global__ void __launch_bounds__(kThreads) k_cache8_expand(const __grid_constan
         w[0][c] = __ldg(reinterpret_cast<const uint2 *>(a.k8 + at) + ch % CPR);
         w[1][c] = __ldg(reinterpret_cast<const uint2 *>(a.v8 + at) + ch % CPR);
         sc[0][c] = __ldg(a.ks + slot), sc[1][c] = __ldg(a.vs + slot);
-        if (sc[1][c] < kMinScale) w[1][c] = make_uint2(0, 0);  // (counts as zeros, as in the kernels over the codes)
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v)
@@ -183,8 +182,7 @@ __global__ void __launch_bounds__(kThreads) k_cache8_expand(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t u = i < 2 ? w[v][c].x : w[v][c].y;
-                const float2 f = e4m3x2_to_float2((u >> (16 * (i & 1))) & 0xFFFFu);
-                r[i] = pack_bf16x2(f.x * sc[v][c], f.y * sc[v][c]);
+                r[i] = e4m3x2_to_bf16x2((u >> (16 * (i & 1))) & 0xFFFFu, sc[v][c]);
             }
             reinterpret_cast<uint4 *>((v ? vo : ko) + (((int64_t)b * a.Hk + hk) * a.Lk + key) * D)[ch % CPR] = make_uint4(r[0], r[1], r[2], r[3]);
         }

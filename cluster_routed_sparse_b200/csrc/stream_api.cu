@@ -42,27 +42,27 @@ constexpr int kMaxLen = 1 << 30;
 // cache after the first time, at a cost that grows with the rows; the tile kernel's is that
 // of 128, and over the cache that of converting every code to 16 bits.  Us of the two,
 // d = 128, few rows / tiles:
-//                                  8 rows       16 rows      32 rows      64 rows
-//   bf16   32,768 keys, 64 heads   166 / 165    281 / 166    541 / 166
-//           2,048 keys, 160 heads   38 / 48      57 / 49      98 / 51
-//           2,048 keys, 8 heads    9.0 / 10.0   9.2 / 10.0   11.6 / 10.2  17.0 / 11.1
-//             320 keys, 2 heads    5.7 / 8.3    5.8 / 8.4    5.9 / 8.4    5.9 / 8.3
-//   8 bits 32,768 keys, 64 heads    97 / 300    171 / 300    319 / 319    599 / 306
-//           2,048 keys, 160 heads   22 / 74      38 / 75      75 / 78     125 / 82
-//             320 keys, 2 heads    6.8 / 9.6    6.8 / 9.4    6.7 / 9.7    6.8 / 10.0
+//                                  8 rows       16 rows      24 rows      32 rows      64 rows
+//   bf16   32,768 keys, 64 heads   166 / 165    281 / 166                 541 / 166
+//           2,048 keys, 160 heads   38 / 48      57 / 49                   98 / 51
+//           2,048 keys, 8 heads    9.0 / 10.0   9.2 / 10.0                11.6 / 10.2  17.0 / 11.1
+//             320 keys, 2 heads    5.7 / 8.3    5.8 / 8.4                 5.9 / 8.4    5.9 / 8.3
+//   8 bits 32,768 keys, 64 heads   110 / 280    200 / 277    281 / 277    371 / 276    698 / 278
+//           2,048 keys, 160 heads   26 / 70      44 / 72      56 / 72      83 / 75     139 / 78
+//             320 keys, 2 heads    9.1 / 10.9   9.3 / 12.1                9.5 / 17.9   9.3 / 11.6
 bool few_rows(const WinArgs &a) {
     const int64_t rows = (int64_t)a.G * a.Lq;
-    return rows <= (a.k8 ? 32 : 8) || (rows <= 64 && window_tiles(a.w, a.Lq, a.Lq, a.Lk, 16) <= 32);
+    return rows <= (a.k8 ? 24 : 8) || (rows <= 64 && window_tiles(a.w, a.Lq, a.Lq, a.Lk, 16) <= 32);
 }
 // Many rows over the cache: its visible part is written out as bf16 once, instead of
 // being converted by every CTA for its 256 rows.  Us of the two, d = 128, codes / bf16:
-//                            512 rows    1,024       1,560       3,120
-//    16,384 keys, 12 heads    76 / 84    133 / 123   242 / 207   447 / 331
-//     8,192 keys, 32 heads   113 / 113   189 / 157   355 / 265   515 / 366
-//     2,048 keys, 8 heads     23 / 24     30 / 30     43 / 38     52 / 42
-//       512 keys, 2 heads     13 / 14     13 / 14     13 / 15     15 / 17   (d = 64)
+//                            512 rows     768         1,024       1,560       3,120
+//    16,384 keys, 12 heads    75 / 87    100 / 107   128 / 131   233 / 219   443 / 367
+//     8,192 keys, 32 heads   102 / 118   147 / 156   173 / 167   321 / 287   481 / 411
+//     2,048 keys, 8 heads     22 / 25     25 / 29     28 / 30     43 / 39     50 / 45
+//       512 keys, 2 heads     12 / 14                 12 / 14     12 / 15     14 / 17   (d = 64)
 // A call that would need more than 1 GiB for it (262,144 tokens of 8 heads) reads the codes.
-constexpr int64_t kExpandRows = 768, kExpandKeys = 16384, kExpandMost = int64_t(1) << 30;
+constexpr int64_t kExpandRows = 1024, kExpandKeys = 16384, kExpandMost = int64_t(1) << 30;
 int64_t expand_bytes(const WinArgs &a) { return (int64_t)a.B * a.Hk * a.Lk * a.d * 4; }
 bool expands(const WinArgs &a) {
     return a.k8 && !few_rows(a) && (int64_t)a.G * a.Lq > kExpandRows && (int64_t)a.B * a.Hk * a.Lk >= kExpandKeys &&

@@ -20,8 +20,8 @@
 //                    zeroes the V rows behind the sequence: 0 x garbage would be NaN)
 //   warp 9           TMEM allocator and tcgen05.mma issuer
 //   8-bit keys: warps 12-15 load the codes of K and warps 16-19 those of V into
-//               registers and store them as fp16 (exact, one conversion for two
-//               codes) in the swizzled layout that the products read.  The codes of
+//               registers and store them, times their pages' scales, as bf16 (exact)
+//               in the swizzled layout that the products read.  The codes of
 //               the next tile are in flight while a thread waits for its stage, and
 //               the scales and page numbers of the ones after that too.  Each thread
 //               keeps its place within 16 rows, so that a tile costs few address
@@ -32,23 +32,18 @@
 // Few query tiles: the key tiles are split over several CTAs, whose partial O
 // and log-sum-exp k_combine joins.
 //
-// Over the 8-bit cache the products are fp16 and the scales stay out of them:
-// Q is multiplied by a power of two per row so that it fits (elements below
-// 2^-14 of the row's largest are off by 2^-25 of it), the scale of K goes into the
-// exponent's factor c, and the scale of V, 2^e, into the exponent itself:
-// P = 2^(S c + e - m) with m the running maximum of S c + e, which keeps P in
-// fp16's range whatever the scales are; the sum takes P 2^-e.
-//
-// Rounding: P to bf16 (fp16 over the cache), the operand type of the product,
-// 2^-9 (2^-12) relative and random over the keys; O once at the end; everything
-// else is fp32.
+// Rounding: P to bf16, the operand type of the product, off by 2^-8 relative at most
+// and random over the keys; over the cache too, because only bf16 has the exponents for
+// weights far below the largest and for pages of very different scales.  (fp16
+// with the scales in the exponents of P loses a weight 2^-25 below the largest one times its
+// page's scale, which the sum still counts.)  O once at the end; everything else is fp32.
 // Bound by the softmax's chain: a pair of row tiles takes 3,500 cycles per key tile (S
 // 1,100 waited for, its load 150, maximum 320, exponentials 1,310, P 285, per row tile)
 // where the products take 2,048.  Frame-causal, 32,760 tokens in frames of 1,560, three
 // frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,020 us alone, 1.14 PFLOP/s, 68%
 // of the measured cuBLAS rate; 1,190 us in a long loop under the power limit.  1,560
 // rows over 18,720 keys, 12 heads (0.18 TFLOP): 204 us; over the codes of the 8-bit cache
-// 295, because every CTA converts them anew and reads its scores twice (registers go to
+// 252, because every CTA converts them anew and reads its scores twice (registers go to
 // the converting threads): many rows take the cache as bf16 rows instead.  Dropped, in us
 // of the two workloads (codes): two threads a row (1,266 in the loop; 595), a quarter of the
 // exponentials as a polynomial on the FMA pipe (no difference), a persistent CTA (1,059
@@ -77,20 +72,18 @@ struct Split {  // threads and registers: bf16 keys launch with 168 each, 8-bit 
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kConverters = 128;  // threads that convert K, and as many V
 
-template <int D, int GROUP>
+template <int D, bool C8>
 struct Layout {
-    static constexpr bool C8 = GROUP != 0;
     static constexpr int HALVES = D / 64;  // 128-byte column halves of a row
     static constexpr uint32_t TILE = HALVES * 128 * 128;
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = 2 * TILE;
     static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
-    static constexpr uint32_t OFF_GRP = OFF_V + NS * TILE;  // [4][8] float4: a tile's groups of 16 keys (8-bit keys)
-    static constexpr uint32_t OFF_ROW = OFF_GRP + (C8 ? 4 * 8 * 16 : 0);  // [2][128] float2: maximum and sum of a row in each warpgroup
+    static constexpr uint32_t OFF_ROW = OFF_V + NS * TILE;  // [2][128] float2: maximum and sum of a row in each warpgroup
     static constexpr uint32_t OFF_BAR = OFF_ROW + (C8 ? 0 : 2 * 128 * 8);
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // 1024-byte alignment slack
 };
-static_assert(Layout<128, 16>::SMEM <= 232448, "shared memory");
+static_assert(Layout<128, false>::SMEM <= 232448, "shared memory");
 
 enum {
     B_KF = 0,     // [NS] K stage filled
@@ -103,8 +96,7 @@ enum {
     B_OF = 15,    // [2] last PV_i complete (MMA commit)
     B_DONE = 17,  // every MMA complete
     B_VZ = 18,    // V rows behind the sequence zeroed (bf16 keys)
-    B_QC = 19,    // query tiles converted to fp16 (8-bit keys)
-    NBAR = 20
+    NBAR = 19
 };
 
 struct WinMaps {
@@ -135,13 +127,11 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *src) {
     return w;
 }
 
-// GROUP: 0 over bf16 keys; over the cache the number of consecutive keys that share
-// their scales, 32 (pages of 32 tokens or more) or 16.
-template <int D, int GROUP>
-__global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
+// C8: over the codes of the 8-bit cache.
+template <int D, bool C8>
+__global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __grid_constant__ WinMaps maps,
                                                             const __grid_constant__ WinParams p) {
-    constexpr bool C8 = GROUP != 0;
-    using LY = Layout<D, GROUP>;
+    using LY = Layout<D, C8>;
     // The half of a tile's keys whose weights come first: over the cache the one that the
     // search for the maximum has read last.
     constexpr int FIRST_HALF = C8 ? 1 : 0;
@@ -206,7 +196,6 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         }
     };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
-    float4 *grp_s = reinterpret_cast<float4 *>(sm + LY::OFF_GRP);
 
     // K and V tiles j of the producer thread
     auto load_tile = [&](bool v, int j) {
@@ -233,7 +222,6 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         mbar_init(BAR(B_QF), 1);
         mbar_init(BAR(B_DONE), 1);
         mbar_init(BAR(B_VZ), 1);
-        mbar_init(BAR(B_QC), has1 ? 2 * BM : BM);
         fence_mbar_init();
         if (n_tiles > 0) {
             const uint32_t bytes = LY::HALVES * p.G * p.TT * 128;
@@ -261,11 +249,11 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
     if (C8 && warp >= 12) {
         reg_dealloc<Split<C8>::CONVERT>();
         if constexpr (C8) {
-            // ------------------------------------------------ 8-bit pages to fp16 tiles
+            // ------------------------------------------------ 8-bit pages to bf16 tiles
             const bool is_v = warp >= 16;
             const int ct = tid & 127, log_t = 31 - __clz(p.T);
             const int *table = p.table + (int64_t)b * p.max_pages;
-            const float *scale_v = p.vs + hk, *scale_k = p.ks + hk;
+            const float *scales = (is_v ? p.vs : p.ks) + hk;
             // A thread converts 16 codes of every 16 RS-th row: row r0 + RS k of a tile, chunk e.
             constexpr int CPR = D / 16, RS = kConverters / CPR, NCH = BN / RS;
             const int r0 = ct / CPR, e = ct % CPR;
@@ -283,10 +271,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 if (entry != -1) atomicOr(&p.err->bits, DEV_ERR_BOUNDS);
                 return -1;
             };
-            auto scales_of = [&](int page, float &ks, float &vs) {
-                ks = page >= 0 ? __ldg(scale_k + (int64_t)page * p.Hk) : 1.f;
-                vs = page >= 0 ? __ldg(scale_v + (int64_t)page * p.Hk) : 1.f;
-            };
+            auto scale_of = [&](int page) { return page >= 0 ? __ldg(scales + (int64_t)page * p.Hk) : 1.f; };
             uint4 w[NCH];
             // Codes of tile j; `page`: of this lane's group of 16 keys.
             auto load = [&](int j, int page) {
@@ -307,11 +292,10 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 // The codes of tile j + 1 are loaded one tile ahead, its scales two, its table entry three:
                 // nothing here waits for a load that was just issued.
                 int entry = entry_of(1), page = page_of(entry_of(0));
-                float ks, vs, ks1, vs1;  // of this lane's page of tile j, and of tile j + 1
-                scales_of(page, ks, vs);
-                load(0, is_v && vs < kMinScale ? -1 : page);
+                float scale = scale_of(page), scale1;  // of this lane's page of tile j, and of tile j + 1
+                load(0, page);
                 page = page_of(entry);
-                scales_of(page, ks1, vs1);
+                scale1 = scale_of(page);
                 entry = entry_of(2);
                 for (int j = 0; j < n_tiles; ++j) {
                     const int s = j % NS;
@@ -319,30 +303,24 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                         ok = false;
                         break;
                     }
-                    if (!is_v && ct < 8) {
-                        // What the softmax needs of the group: the scale of K, the exponent of the
-                        // scale of V and its inverse.  (The slot's last readers are four tiles back.)
-                        const float ev = fmaxf(__log2f(vs), kMinLogScale);
-                        grp_s[(j & 3) * 8 + ct] = make_float4(ks, ev, ex2_approx(-ev), 0.f);
-                    }
                     uint8_t *d = dst + s * LY::TILE;
 #pragma unroll
                     for (int k = 0; k < NCH; ++k) {
+                        const float f = __shfl_sync(0xFFFFFFFFu, scale, (r0 + RS * k) >> 4);
                         *reinterpret_cast<uint4 *>(d + k * RS * 128 + sw0) =
-                            make_uint4(e4m3x2_to_half2(w[k].x & 0xFFFFu), e4m3x2_to_half2(w[k].x >> 16),
-                                       e4m3x2_to_half2(w[k].y & 0xFFFFu), e4m3x2_to_half2(w[k].y >> 16));
+                            make_uint4(e4m3x2_to_bf16x2(w[k].x & 0xFFFFu, f), e4m3x2_to_bf16x2(w[k].x >> 16, f),
+                                       e4m3x2_to_bf16x2(w[k].y & 0xFFFFu, f), e4m3x2_to_bf16x2(w[k].y >> 16, f));
                         *reinterpret_cast<uint4 *>(d + k * RS * 128 + sw1) =
-                            make_uint4(e4m3x2_to_half2(w[k].z & 0xFFFFu), e4m3x2_to_half2(w[k].z >> 16),
-                                       e4m3x2_to_half2(w[k].w & 0xFFFFu), e4m3x2_to_half2(w[k].w >> 16));
+                            make_uint4(e4m3x2_to_bf16x2(w[k].z & 0xFFFFu, f), e4m3x2_to_bf16x2(w[k].z >> 16, f),
+                                       e4m3x2_to_bf16x2(w[k].w & 0xFFFFu, f), e4m3x2_to_bf16x2(w[k].w >> 16, f));
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(BAR((is_v ? B_VF : B_KF) + s));
                     if (j + 1 < n_tiles) {
-                        // (a V page whose scale is below 2^-90 counts as zeros)
-                        load(j + 1, is_v && vs1 < kMinScale ? -1 : page);
-                        ks = ks1, vs = vs1;
+                        load(j + 1, page);
+                        scale = scale1;
                         page = page_of(entry);
-                        scales_of(page, ks1, vs1);
+                        scale1 = scale_of(page);
                         entry = entry_of(j + 3);
                     }
                 }
@@ -356,9 +334,8 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
             // (the whole warp, with the same values in every lane: see stream_device.cuh)
             const int n = uniform(n_tiles), two = uniform(has1), solo = uniform(!pair), turn = solo ? 2 : 1, clean = uniform(tail);
             if (n > 0) {
-                constexpr uint32_t kTypes = C8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 or bf16 operands
-                constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false) & kTypes;
-                constexpr uint32_t IPV = idesc_bf16_f32(BM, D, true) & kTypes;
+                constexpr uint32_t IQK = idesc_bf16_f32(BM, BN, false);
+                constexpr uint32_t IPV = idesc_bf16_f32(BM, D, true);
                 constexpr uint32_t STEP = LY::TILE >> 4;
                 const uint32_t leader = elect_one();
                 const Desc dq0 = make_desc(sdesc_sw128(sbase + LY::OFF_Q, 16, 1024));
@@ -375,7 +352,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     mma_weights<64>(leader, 256 + i * 128, i * BN, Desc{dv0.lo + (j % NS) * STEP, dv0.hi}, IPV,
                                     j >= turn || h != FIRST_HALF ? 1u : 0u, h);
                 };
-                bool go = wait_all(C8 ? B_QC : B_QF, 0) && wait_all(B_KF, 0);
+                bool go = wait_all(B_QF, 0) && wait_all(B_KF, 0);
                 tc_fence_after();
                 if (go) {
                     issue_s(0, 0);
@@ -477,41 +454,10 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
         const bool active = C8 ? n_tiles > 0 && (wg == 0 || has1) : n_tiles > (has1 ? 0 : wg);
         float2 *row_s = reinterpret_cast<float2 *>(sm + LY::OFF_ROW);
         if (active) {
-            float sl2 = p.scale_log2;
-            if (C8) {
-                // This thread's row of Q to fp16, scaled by a power of two to below 2.
-                if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_QF), 0))) ok = false;
-                uint8_t *qrow = sm + LY::OFF_Q + wg * LY::TILE + row * 128;
-                uint32_t top = 0;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(qrow + (c / 8) * BM * 128 + (((c % 8) ^ (row & 7)) << 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-                }
-                const int ex = top ? min(max((int)(top >> 7) - 127, -120), 120) : 0;
-                const float dn = exp2i(-ex);
-                sl2 *= exp2i(ex);
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 *at = reinterpret_cast<uint4 *>(qrow + (c / 8) * BM * 128 + (((c % 8) ^ (row & 7)) << 4));
-                    const uint4 w = *at;
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = pack_half2(__uint_as_float(u[e] << 16) * dn, __uint_as_float(u[e] & 0xFFFF0000u) * dn);
-                    *at = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(BAR(B_QC));
-            }
+            const float sl2 = p.scale_log2;
             for (int j = pair ? 0 : wg; j < n_tiles && ok; j += step) {
                 // Wait outcomes are combined across the warp: the TMEM loads and
                 // stores below are warp-collective, so a warp leaves together.
-                // (Over the cache S also tells that the tile's groups are there: they were stored
-                // before K was, which S waited for.  A wait for K itself could miss its phase:
-                // K of tile j + 2 may be there already.)
                 if (!__all_sync(0xFFFFFFFFu, wait(BAR(B_SF + wg), (pair ? j : j >> 1) & 1))) {
                     ok = false;
                     break;
@@ -541,30 +487,16 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                         }
                     }
                 };
-                const float4 *grp = grp_s + (j & 3) * 8;  // of 16 keys each (over the cache)
-                // (never 0: a masked column is -inf times it)
-                auto factor = [&](float ks) { return fmaxf(sl2 * ks, 1e-37f); };
                 float m_new = m_run;
                 auto maximum = [&](int h) {
                     const uint32_t(&x)[2][32] = r[h % KEEP];
-                    // four independent ones, over the cache those of the groups
-                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four independent ones)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int a = !C8 ? (e >> 1) & 3 : 2 * c + (GROUP == 16 ? e >> 4 : (e >> 1) & 1);
-                            pm[a] = fmax3(pm[a], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-                        }
-                    if (!C8) {
-                        m_new = fmaxf(m_new, fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3])) * sl2);
-                    } else {
-#pragma unroll
-                        for (int a = 0; a < 64 / (C8 ? GROUP : 64); ++a) {
-                            const float4 f = grp[h * 4 + a * (GROUP / 16)];
-                            m_new = fmaxf(m_new, fmaf(GROUP == 16 ? pm[a] : fmaxf(pm[2 * a], pm[2 * a + 1]), factor(f.x), f.y));
-                        }
-                    }
+                        for (int e = 0; e < 32; e += 2)
+                            pm[(e >> 1) & 3] = fmax3(pm[(e >> 1) & 3], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                    m_new = fmaxf(m_new, fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3])) * sl2);
                 };
                 if (C8) {
 #pragma unroll 1
@@ -602,7 +534,7 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;  // nothing seen yet: every p is 0
                 auto weights = [&](int h) {
                     const uint32_t(&x)[2][32] = r[h % KEEP];
-                    uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
+                    const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m_use, -m_use);
                     uint64_t ps2[4];
 #pragma unroll
                     for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
@@ -611,32 +543,17 @@ __global__ void __launch_bounds__(Split<GROUP != 0>::THREADS, 1) k_window_attn(c
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            if (C8 && e % (C8 ? GROUP : 32) == 0) {
-                                const float4 f = grp[h * 4 + 2 * c + e / 16];
-                                const float k = factor(f.x), n = f.y - m_use;
-                                sl2x2 = f2_pack(k, k), negm2 = f2_pack(n, n);
-                            }
                             const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sl2x2, negm2);
                             float p0, p1;
                             f2_unpack(x2, p0, p1);
                             p0 = ex2_approx(p0), p1 = ex2_approx(p1);
                             ps2[(e >> 1) & 3] = f2_add(ps2[(e >> 1) & 3], f2_pack(p0, p1));
-                            pk[c * 16 + (e >> 1)] = C8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
-                            if (C8 && e % (C8 ? GROUP : 32) == (C8 ? GROUP : 32) - 2) {
-                                // the sum takes P without the scale of V
-                                float a0, a1;
-                                f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
-                                l_run = fmaf(a0 + a1, grp[h * 4 + 2 * c + e / 16].z, l_run);
-#pragma unroll
-                                for (int a = 0; a < 4; ++a) ps2[a] = f2_pack(0.f, 0.f);
-                            }
+                            pk[c * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
                         }
                     tmem_st32(tS + h * 64, pk);
-                    if (!C8) {
-                        float a0, a1;
-                        f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
-                        l_run += a0 + a1;
-                    }
+                    float a0, a1;
+                    f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), a0, a1);
+                    l_run += a0 + a1;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -891,15 +808,10 @@ cudaError_t launch_window_mma(const WinArgs &a, cudaStream_t s) {
         AC_NOTE_LAUNCH();
         return cudaGetLastError();
     };
-    const int group = !a.k8 ? 0 : a.T == 16 ? 16 : 32;
     if (a.d == 128)
-        e = group == 0    ? go(k_window_attn<128, 0>, Layout<128, 0>::SMEM)
-            : group == 16 ? go(k_window_attn<128, 16>, Layout<128, 16>::SMEM)
-                          : go(k_window_attn<128, 32>, Layout<128, 32>::SMEM);
+        e = a.k8 ? go(k_window_attn<128, true>, Layout<128, true>::SMEM) : go(k_window_attn<128, false>, Layout<128, false>::SMEM);
     else
-        e = group == 0    ? go(k_window_attn<64, 0>, Layout<64, 0>::SMEM)
-            : group == 16 ? go(k_window_attn<64, 16>, Layout<64, 16>::SMEM)
-                          : go(k_window_attn<64, 32>, Layout<64, 32>::SMEM);
+        e = a.k8 ? go(k_window_attn<64, true>, Layout<64, true>::SMEM) : go(k_window_attn<64, false>, Layout<64, false>::SMEM);
     if (e != cudaSuccess || pl.nsplit == 1) return e;
     return launch_combine(p.part_o, p.part_lse, a, pl.nsplit, s);
 }

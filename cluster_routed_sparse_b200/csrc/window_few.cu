@@ -16,13 +16,21 @@
 //
 // One token of four sequences over 16,384 of 32,760 bf16 keys and 128 first ones, 40
 // heads (1.35 GB): 209 us in a graph, the rate of a copy.  One token of eight sequences
-// over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 93 us, 5.8 TB/s, 90% of it;
-// the rest is the joining launch and the last wave.  More rows take as many CTAs, which
-// find the keys in the L2 cache: 171 us for 16 rows over that cache (in one CTA: 183, the
-// registers then leave three of them on an SM), 319 for 32.
+// over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 106 us, 5.1 TB/s, 79% of it:
+// a warp waits for its loads and then works, and converting V to bf16 takes 8 us of that,
+// the second part of the weights 3 (fp16 codes and weights took 95, and lost weights;
+// integer steps instead of the two conversions 116; 5 CTAs on an SM spill, 152).
+// More rows take as many CTAs, which find the keys in the L2 cache: 200 us for 16 rows over
+// a cache of that size, 281 for 24.
 //
-// Types, scales and roundings as in the tile kernel: bf16 over bf16 keys, fp16 with
-// the scales in the exponents over the 8-bit cache.
+// Over the 8-bit cache K enters its product as fp16 codes (one conversion for two of them), with
+// the scale of its page taken into the scores and Q divided by a power of two per row to fit
+// (elements below 2^-14 of the row's largest are off by 2^-25 of it), and V as bf16 codes.
+// Rounding: a weight is a sum of two bf16 values, hence off by 2^-17 at most, over
+// fp32's whole range of exponents; over the cache it takes the scale of V's page first, a power of
+// two, and the sum of the weights does without.  (In fp16 small weights lost their bits
+// beside a page of large values.)  The second value's products are hidden behind the loads.
+// O is rounded once at the end; everything else is fp32.
 #include "stream_device.cuh"
 
 namespace ac {
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
         }
         if (more) load_k(nxt, base2);
 
-        // scores in log2 units
+        // scores in log2 units, without V's scale
         bool full = true;
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
@@ -243,12 +251,11 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
                     x = key < rr[e].hi && (key >= rr[e].lo || key < sink[e]) ? x : -INFINITY;
                 }
         }
-        const float ev = C8 ? fmaxf(__log2f(vs), kMinLogScale) : 0.f;  // exponent of the scale of V
         float top[NR];
         bool grows = false;
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
-            top[e] = ev + fmaxf(s[e], s[2 + e]);
+            top[e] = fmaxf(s[e], s[2 + e]);
             grows = grows || top[e] > m[e] + 8.f;
         }
         // The maximum moves when some row's grew by more than 2^8 (or is the first).
@@ -267,36 +274,46 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
             }
         }
         // weights, and P^T as the B operand: keys 8 u + 2 t4 + {0, 1} of row g8
-        const float inv_vs = C8 ? ex2_approx(-ev) : 1.f;
-        uint32_t bp[2];
+        uint32_t bp[2][2];  // [high and low part][u]
         float pr[2][2];
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
-            const float mu = (m[e] == -INFINITY ? 0.f : m[e]) - ev;
+            const float mu = m[e] == -INFINITY ? 0.f : m[e];
             pr[0][e] = ex2_approx(s[e] - mu), pr[1][e] = ex2_approx(s[2 + e] - mu);
-            const float sum = pr[0][e] + pr[1][e];
-            l[e] = C8 ? fmaf(sum, inv_vs, l[e]) : l[e] + sum;
+            l[e] += pr[0][e] + pr[1][e];
+            if (C8) pr[0][e] *= vs, pr[1][e] *= vs;
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) bp[u] = transpose8x8(C8 ? pack_half2(pr[u][0], pr[u][1]) : pack_bf16x2(pr[u][0], pr[u][1]));
-        // O^T: row g8 of m16 tile n is element g8 D/8 + 2 n, row g8 + 8 the next one.  (Values in a
-        // page with a scale below 2^-90 count as zeros.)
-        if (!C8 || vs >= kMinScale) {
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t hi = pack_bf16x2(pr[u][0], pr[u][1]);
+            bp[0][u] = transpose8x8(hi);
+            bp[1][u] = transpose8x8(pack_bf16x2(pr[u][0] - __uint_as_float(hi << 16), pr[u][1] - __uint_as_float(hi & 0xFFFF0000u)));
+        }
+        // O^T: row g8 of m16 tile n is element g8 D/8 + 2 n, row g8 + 8 the next one.
+        // Four tiles at a time: the products of a weight's two parts, which add up in one
+        // accumulator, stand apart (one token over 32,760 cached tokens, 64 heads: 114 us side by side, 106).
+        constexpr int GRP = 4;
 #pragma unroll
-            for (int n = 0; n < DT; ++n) {
-                uint32_t a[4];
+        for (int n0 = 0; n0 < DT; n0 += GRP) {
+            uint32_t a[GRP][4];
+#pragma unroll
+            for (int i = 0; i < GRP; ++i) {
+                const int n = n0 + i;
                 if constexpr (C8) {
                     const int word = n / 2;  // bytes 2 n, 2 n + 1 of the four rows
                     const uint32_t sel = n & 1 ? 0x7362 : 0x5140;
                     const uint32_t x = __byte_perm(vw[0][word], vw[1][word], sel), y = __byte_perm(vw[2][word], vw[3][word], sel);
-                    a[0] = e4m3x2_to_half2(x & 0xFFFFu), a[1] = e4m3x2_to_half2(x >> 16);
-                    a[2] = e4m3x2_to_half2(y & 0xFFFFu), a[3] = e4m3x2_to_half2(y >> 16);
+                    a[i][0] = e4m3x2_to_bf16x2(x & 0xFFFFu), a[i][1] = e4m3x2_to_bf16x2(x >> 16);
+                    a[i][2] = e4m3x2_to_bf16x2(y & 0xFFFFu), a[i][3] = e4m3x2_to_bf16x2(y >> 16);
                 } else {
-                    a[0] = __byte_perm(vw[0][n], vw[1][n], 0x5410), a[1] = __byte_perm(vw[0][n], vw[1][n], 0x7632);
-                    a[2] = __byte_perm(vw[2][n], vw[3][n], 0x5410), a[3] = __byte_perm(vw[2][n], vw[3][n], 0x7632);
+                    a[i][0] = __byte_perm(vw[0][n], vw[1][n], 0x5410), a[i][1] = __byte_perm(vw[0][n], vw[1][n], 0x7632);
+                    a[i][2] = __byte_perm(vw[2][n], vw[3][n], 0x5410), a[i][3] = __byte_perm(vw[2][n], vw[3][n], 0x7632);
                 }
-                mma<C8>(acc[n], a[0], a[1], a[2], a[3], bp[0], bp[1]);
             }
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int i = 0; i < GRP; ++i) mma<false>(acc[n0 + i], a[i][0], a[i][1], a[i][2], a[i][3], bp[part][0], bp[part][1]);
         }
         if (more) load_v(nxt, base2);
         ks = ks_next, vs = vs_next;

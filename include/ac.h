@@ -522,11 +522,9 @@ AC_API ac_status ac_cache8_append(const ac_cache8 *cache, const ac_view *k, cons
 /* ac_window_attn over the cache: q, o [B, Hq, Lq, d] bf16, k_lens (device int32
  * [B]) the tokens in the cache.  Pages that no query sees are not read, their
  * table entries may be anything; a visible page whose index is out of range
- * reads as zeros (AC_ERR_BOUNDS).  Values in pages with a scale below 2^-90
- * count as zeros.  The NaN codes of a cache behind its sequences do no harm; one
- * within makes the rows that see it NaN (a value that element of theirs, and of rows
- * near them that do not).  With
- * many query rows the workspace holds the visible keys and values in 16 bits too
+ * reads as zeros (AC_ERR_BOUNDS).  The NaN codes of a cache behind its sequences do
+ * no harm; one within makes the rows that see it NaN (a value: that element of theirs, and
+ * of rows near them that do not).  With many query rows the workspace holds the visible keys and values in 16 bits too
  * (max_pages page_tokens tokens of every sequence, where that is at most 1 GiB). */
 AC_API ac_status ac_cache8_attn_workspace(const ac_cache8 *cache, int32_t B, int32_t Hq, int32_t Lq,
                                           int32_t max_pages, const ac_window *w, int64_t *bytes);
