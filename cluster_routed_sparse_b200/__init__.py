@@ -10,7 +10,7 @@ call does, and fails loudly if libac.so is missing.
 """
 
 _STREAMING = ("rope_axes", "window_attn", "window_attn_backward", "Cache8", "cache8_append", "cache8_attn",
-              "ops_status")
+              "ops_status", "ops_check_wait_timeout")
 
 __all__ = ["SparseLayer", "synth", *_STREAMING]
 

@@ -136,6 +136,7 @@ SIGNATURES = {
     "ac_cache8_attn_workspace": (_I, [_C8, _I, _I, _I, _I, _WN, _I64P]),
     "ac_cache8_attn": (_I, [_C8, _VW, _VW, _P, _I, _I, _I, _P, _I, _P, _P, _WN, _P, ctypes.c_int64, _P]),
     "ac_ops_status": (_I, [_P]),
+    "ac_ops_check_wait_timeout": (_I, [_I, _P]),
 }
 
 _lib = None

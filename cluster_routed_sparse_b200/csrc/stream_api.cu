@@ -168,6 +168,27 @@ uint32_t ac::next_launch_id() {
     return id;
 }
 
+namespace {
+__global__ void k_ops_wait_check(OpErr *err, uint32_t launch, uint64_t limit_ns) {
+    __shared__ alignas(8) uint64_t bar;
+    mbar_init(smem_u32(&bar), 1);
+    fence_mbar_init();
+    wait_or_note(smem_u32(&bar), 0, &err->timeout, launch, limit_ns);
+}
+}  // namespace
+
+extern "C" ac_status ac_ops_check_wait_timeout(int32_t limit_us, void *stream) {
+    if (limit_us < 1 || limit_us > 2000000) return refuse("ac_ops_check_wait_timeout: limit_us outside 1 .. 2,000,000");
+    OpErr *p = nullptr;
+    cudaError_t e = op_err_address(&p);
+    if (e == cudaSuccess) {
+        k_ops_wait_check<<<1, 1, 0, (cudaStream_t)stream>>>(p, next_launch_id(), (uint64_t)limit_us * 1000ull);
+        AC_NOTE_LAUNCH();
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? AC_OK : cuda_refuse("ac_ops_check_wait_timeout", e);
+}
+
 extern "C" ac_status ac_ops_status(void *stream) {
     OpErr *p = nullptr, h;
     cudaStream_t s = (cudaStream_t)stream;

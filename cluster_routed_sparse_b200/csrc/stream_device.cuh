@@ -41,6 +41,26 @@ __device__ __forceinline__ int seq_len(const int *lens, int b, int most, OpErr *
     return n < 0 ? 0 : n > most ? most : n;
 }
 
+// Bounded wait of a launch's kernels.  The first to expire notes the launch, which ends the
+// others' waits early.  What is in flight when a wait gives up is waited for with mbar_wait,
+// which does not look at that note: loads and products issued end by themselves.
+__device__ __forceinline__ bool wait_or_note(uint32_t bar, uint32_t parity, uint32_t *noted, uint32_t launch,
+                                             uint64_t limit_ns = kWaitLimitNs) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    const long long c0 = clock64(), limit_cycles = (long long)limit_ns * 2;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 255u) {
+            if (*reinterpret_cast<const volatile uint32_t *>(noted) == launch) return false;
+            if (globaltimer_ns() - t0 > limit_ns || clock64() - c0 > limit_cycles || it > kWaitLimitPolls) {
+                *reinterpret_cast<volatile uint32_t *>(noted) = launch;
+                return false;
+            }
+        }
+    }
+}
+
 // 5-D tiled bulk tensor load (coordinates x innermost).  No cluster multicast.
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int32_t x, int32_t y, int32_t z, int32_t w,
                                             int32_t v, uint32_t bar) {

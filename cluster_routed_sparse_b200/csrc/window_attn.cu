@@ -51,8 +51,8 @@
 // (1,215 in the loop; 341), each converting register refilled as soon as it is free (17 rows:
 // 258 -> 290).
 //
-// Every mbarrier wait is bounded; on timeout the CTA notes it, drains what it
-// issued and frees its TMEM.
+// Every mbarrier wait is bounded; on timeout the CTA notes it, waits for the loads and
+// products that it issued (for a bounded time too) and frees its TMEM.
 #include <type_traits>
 
 #include "stream_device.cuh"
@@ -178,23 +178,7 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
 
     const uint32_t bar0 = sbase + LY::OFF_BAR;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
-    uint32_t *abort_word = &p.err->timeout;
-    // Bounded wait; the first to expire notes the launch, which ends the others' waits early.
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
-        const long long c0 = clock64();
-        for (uint32_t it = 0;; ++it) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((it & 255u) == 255u) {
-                if (*reinterpret_cast<const volatile uint32_t *>(abort_word) == p.launch) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs || clock64() - c0 > kWaitLimitCycles || it > kWaitLimitPolls) {
-                    *reinterpret_cast<volatile uint32_t *>(abort_word) = p.launch;
-                    return false;
-                }
-            }
-        }
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_or_note(bar, parity, &p.err->timeout, p.launch); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
 
     // K and V tiles j of the producer thread
@@ -390,7 +374,7 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                     commit(leader, BAR(B_VE + j % NS));
                 }
                 commit(leader, BAR(B_DONE));
-                wait(BAR(B_DONE), 0);
+                mbar_wait(BAR(B_DONE), 0);
             }
             __syncwarp();
         } else if (warp == 8 && lane == 0 && n_tiles > 0) {
@@ -413,9 +397,9 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                     }
                 }
                 // Loads still in flight must land before the CTA exits.
-                for (int j = max(kd - NS, 0); j < kd; ++j) wait(BAR(B_KF + j % NS), (j / NS) & 1);
-                for (int j = max(vd - NS, 0); j < vd; ++j) wait(BAR(B_VF + j % NS), (j / NS) & 1);
-                wait(BAR(B_QF), 0);
+                for (int j = max(kd - NS, 0); j < kd; ++j) mbar_wait(BAR(B_KF + j % NS), (j / NS) & 1);
+                for (int j = max(vd - NS, 0); j < vd; ++j) mbar_wait(BAR(B_VF + j % NS), (j / NS) & 1);
+                mbar_wait(BAR(B_QF), 0);
             }
         }
         if (!C8 && warp == 8 && tail) {
@@ -423,7 +407,7 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
             __syncwarp();
             const int j = n_tiles - 1, s = j % NS, r0 = kl - tile_base(j);
             if (__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
-                wait(BAR(B_VF + s), (j / NS) & 1);
+                mbar_wait(BAR(B_VF + s), (j / NS) & 1);
                 for (int hf = 0; hf < LY::HALVES; ++hf)
                     for (int i = r0 * 8 + lane; i < BN * 8; i += 32)
                         *reinterpret_cast<uint4 *>(sm + LY::OFF_V + s * LY::TILE + hf * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
@@ -432,7 +416,7 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
                 if (lane == 0) mbar_arrive(BAR(B_VZ));
             }
         }
-        if (C8 && warp == 8 && lane == 0 && n_tiles > 0) wait(BAR(B_QF), 0);  // in flight until then
+        if (C8 && warp == 8 && lane == 0 && n_tiles > 0) mbar_wait(BAR(B_QF), 0);  // in flight until then
         __syncwarp();
     } else {
         reg_alloc<Split<C8>::SOFTMAX>();

@@ -238,22 +238,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
 
     const uint32_t bar0 = sbase + LY::OFF_BAR;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
-    uint32_t *abort_word = &p.err->timeout;
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
-        const long long c0 = clock64();
-        for (uint32_t it = 0;; ++it) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((it & 255u) == 255u) {
-                if (*reinterpret_cast<const volatile uint32_t *>(abort_word) == p.launch) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs || clock64() - c0 > kWaitLimitCycles || it > kWaitLimitPolls) {
-                    *reinterpret_cast<volatile uint32_t *>(abort_word) = p.launch;
-                    return false;
-                }
-            }
-        }
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_or_note(bar, parity, &p.err->timeout, p.launch); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
 
     const int packed = p.G * p.TT;  // rows of a query tile
@@ -392,7 +377,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
                     }
                 }
                 commit(leader, BAR(B_AF));
-                wait(BAR(B_AF), 0);
+                mbar_wait(BAR(B_AF), 0);
             }
         } else if (warp == 8 && n_tiles > 0) {
           if (lane == 0) {
@@ -408,8 +393,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             }
             // Loads still in flight must land before the CTA exits.
             for (int t = 0; t < 2; ++t)
-                for (int j = max(done[t] - 2, 0); j < done[t]; ++j) wait(BAR((t ? B_1F : B_0F) + (j & 1)), (j >> 1) & 1);
-            wait(BAR(B_FF), 0);
+                for (int j = max(done[t] - 2, 0); j < done[t]; ++j) mbar_wait(BAR((t ? B_1F : B_0F) + (j & 1)), (j >> 1) & 1);
+            mbar_wait(BAR(B_FF), 0);
           }
           __syncwarp();
           if (tail && __shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
@@ -417,7 +402,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) k_window_bwd(const __grid_constan
             // (by the producer, which has followed every phase of the stages)
             const int j = n_tiles - 1, s = j & 1;
             for (int t = 0; t < 2; ++t) {
-                wait(BAR((t ? B_1F : B_0F) + s), (j >> 1) & 1);
+                mbar_wait(BAR((t ? B_1F : B_0F) + s), (j >> 1) & 1);
                 for (int hf = 0; hf < LY::HALVES; ++hf)
                     for (int i = max(tail_row, 0) * 8 + lane; i < 128 * 8; i += 32)
                         *reinterpret_cast<uint4 *>(sm + (t ? LY::OFF_L1 : LY::OFF_L0) + s * LY::TILE + hf * 128 * 128 + i * 16) =

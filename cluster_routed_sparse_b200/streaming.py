@@ -8,6 +8,7 @@ video generator that works frame after frame.
                             a paged cache of keys and values in 8 bits, and the
                             attention that reads it
     ops_status              waits, and raises what the kernels have noted
+    ops_check_wait_timeout  health check of that: a wait that runs out
 
 Each call forwards data pointers, strides and the current stream of the
 tensors' device to the C ABI in include/ac.h, which documents the operators;
@@ -377,7 +378,16 @@ def ops_status(device=None):
     """Wait for the current stream of `device` and raise ACError for what kernels of
     these operators have noted there since the last call: a length or page index
     out of range (AC_ERR_BOUNDS) or an expired wait (AC_ERR_TIMEOUT)."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    if dev.type == "cuda" and dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    _on(dev, _lib.load().ac_ops_status)
+    _on(_cuda_device(device), _lib.load().ac_ops_status)
+
+
+def ops_check_wait_timeout(limit_us: int, device=None):
+    """Enqueue the bounded-wait health check of these operators
+    (ac_ops_check_wait_timeout); the next ops_status raises with AC_ERR_TIMEOUT."""
+    dev, fn = _cuda_device(device), _lib.load().ac_ops_check_wait_timeout
+    _on(dev, functools.partial(fn, int(limit_us)))
+
+
+def _cuda_device(device):
+    dev = torch.device("cuda" if device is None else device)
+    return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev

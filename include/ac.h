@@ -538,6 +538,12 @@ AC_API ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, const 
  * AC_ERR_BOUNDS. */
 AC_API ac_status ac_ops_status(void *stream);
 
+/* Health check of that path, as ac_check_wait_timeout is the layer's: on `stream` one
+ * thread waits, with the loop of these operators' kernels, for a phase that never
+ * completes, at most limit_us microseconds (1 .. 2,000,000); the next ac_ops_status
+ * reports AC_ERR_TIMEOUT.  Errors: INVALID_ARG, CUDA. */
+AC_API ac_status ac_ops_check_wait_timeout(int32_t limit_us, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
