@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <thread>
 
 #include "stream_device.cuh"
 
@@ -189,19 +190,53 @@ extern "C" ac_status ac_ops_check_wait_timeout(int32_t limit_us, void *stream) {
     return e == cudaSuccess ? AC_OK : cuda_refuse("ac_ops_check_wait_timeout", e);
 }
 
+// What was noted is taken and cleared in one step, so that no note of another stream's kernels
+// gets lost in between.  An expired wait comes first; the bits then stay for the next call.
+namespace {
+constexpr int kSlots = 64;  // calls at once
+__device__ OpErr g_taken[kSlots];
+std::atomic<uint64_t> g_slots{0};  // those in use
+
+__global__ void k_ops_take(OpErr *err, int slot) {
+    OpErr t{atomicExch(&err->timeout, 0u), 0u};
+    if (!t.timeout) t.bits = atomicExch(&err->bits, 0u);
+    g_taken[slot] = t;
+}
+
+struct Slot {
+    int i;
+    Slot() {
+        uint64_t used = g_slots.load(std::memory_order_relaxed);
+        for (;;) {
+            if (used == ~uint64_t(0)) {
+                std::this_thread::yield();
+                used = g_slots.load(std::memory_order_relaxed);
+                continue;
+            }
+            i = __builtin_ctzll(~used);
+            if (g_slots.compare_exchange_weak(used, used | uint64_t(1) << i, std::memory_order_acquire)) return;
+        }
+    }
+    ~Slot() { g_slots.fetch_and(~(uint64_t(1) << i), std::memory_order_release); }
+};
+}  // namespace
+
 extern "C" ac_status ac_ops_status(void *stream) {
-    OpErr *p = nullptr, h;
+    OpErr *p = nullptr, h{};
+    void *taken = nullptr;
     cudaStream_t s = (cudaStream_t)stream;
+    const Slot slot;
     cudaError_t e = op_err_address(&p);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(&h, p, sizeof(h), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&taken, g_taken);
+    if (e == cudaSuccess) {
+        k_ops_take<<<1, 1, 0, s>>>(p, slot.i);
+        AC_NOTE_LAUNCH();
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&h, static_cast<OpErr *>(taken) + slot.i, sizeof(h), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_refuse("ac_ops_status", e);
-    if (h.timeout || h.bits) {
-        e = cudaMemsetAsync(p, 0, sizeof(h), s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        if (e != cudaSuccess) return cuda_refuse("ac_ops_status", e);
-    }
-    if (h.timeout || (h.bits & DEV_ERR_TIMEOUT)) return refuse("a bounded in-kernel wait expired", AC_ERR_TIMEOUT);
+    if (h.timeout) return refuse("a bounded in-kernel wait expired", AC_ERR_TIMEOUT);
     if (h.bits) return refuse("a length or a page index on the device is out of range", AC_ERR_BOUNDS);
     return AC_OK;
 }

@@ -535,7 +535,8 @@ AC_API ac_status ac_cache8_attn(const ac_cache8 *cache, const ac_view *q, const 
 
 /* Waits for `stream` and reports what kernels of the streaming operators on the
  * current device have noted since the last call: AC_OK, AC_ERR_TIMEOUT or
- * AC_ERR_BOUNDS. */
+ * AC_ERR_BOUNDS (in that order, one in each call).  What other streams' kernels note
+ * meanwhile is kept for the next call. */
 AC_API ac_status ac_ops_status(void *stream);
 
 /* Health check of that path, as ac_check_wait_timeout is the layer's: on `stream` one
