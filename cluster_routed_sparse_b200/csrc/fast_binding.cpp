@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "ac.h"
@@ -79,50 +80,43 @@ PyObject *two(const Tensor &a, const Tensor &b) {
     return t;
 }
 
-#define CATCH                                       \
-    catch (const std::exception &e) {               \
-        PyErr_SetString(PyExc_RuntimeError, e.what()); \
-        return nullptr;                             \
-    }
-
 // rope(q, k, positions, freq address, pairs address, axes, pairs' sum, interleaved, inverse)
 PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    try {
-        int64_t i[6];
-        if (n != 9 || !integers(args + 3, 6, i)) return none();
-        const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *pos = tensor(args[2]);
-        if (!q || !pos || !q->is_cuda() || (!k && args[1] != Py_None)) return none();
-        const c10::DeviceIndex dev = q->get_device();
-        if (dev != c10::cuda::current_device()) return none();
-        const at::ScalarType type = q->scalar_type();
-        const int32_t dtype = type == at::kBFloat16 ? AC_DTYPE_BF16 : type == at::kHalf ? AC_DTYPE_F16 : type == at::kFloat ? AC_DTYPE_F32 : -1;
-        ac_view vq, vk{}, oq, ok{};
-        if (dtype < 0 || !rows(*q, type, dev, &vq)) return none();
-        const int64_t B = q->size(0), Hq = q->size(1), L = q->size(2), d = q->size(3), axes = i[2];
-        int64_t Hk = 0;
-        if (k) {
-            if (!rows(*k, type, dev, &vk)) return none();
-            Hk = k->size(1);
-            if (!same(*k, B, Hk, L, d)) return none();
-        }
-        if (!on(*pos, at::kInt, dev) || !pos->is_contiguous()) return none();
-        const bool per_sequence = pos->dim() == 3;
-        if (per_sequence ? pos->size(0) != B || pos->size(1) != L || pos->size(2) != axes
-                         : pos->dim() != 2 || pos->size(0) != L || pos->size(1) != axes)
-            return none();
-        if (!fits(B) || !fits(Hq) || !fits(Hk) || !fits(L) || !fits(d)) return none();
-        const Tensor yq = like(*q, {B, Hq, L, d}, type);
-        const Tensor yk = k ? like(*k, {B, Hk, L, d}, type) : Tensor();
-        oq = ac_view{yq.data_ptr(), Hq * L * d, L * d, d};
-        if (k) ok = ac_view{yk.data_ptr(), Hk * L * d, L * d, d};
-        const ac_status st = ac_rope_axes(dtype, &vq, &oq, (int32_t)Hq, &vk, &ok, (int32_t)Hk, (int32_t)B, (int32_t)L, (int32_t)d,
-                                          static_cast<const int32_t *>(pos->data_ptr()), per_sequence ? L * axes : 0,
-                                          reinterpret_cast<const double *>(i[0]), reinterpret_cast<const int32_t *>(i[1]),
-                                          (int32_t)axes, i[4] != 0, i[5] != 0, stream(dev));
-        if (st != AC_OK) return error(st);
-        return k ? two(yq, yk) : THPVariable_Wrap(yq);
+    HANDLE_TH_ERRORS  // (torch's own exceptions: out of memory is torch.OutOfMemoryError)
+    int64_t i[6];
+    if (n != 9 || !integers(args + 3, 6, i)) return none();
+    const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *pos = tensor(args[2]);
+    if (!q || !pos || !q->is_cuda() || (!k && args[1] != Py_None)) return none();
+    const c10::DeviceIndex dev = q->get_device();
+    if (dev != c10::cuda::current_device()) return none();
+    const at::ScalarType type = q->scalar_type();
+    const int32_t dtype = type == at::kBFloat16 ? AC_DTYPE_BF16 : type == at::kHalf ? AC_DTYPE_F16 : type == at::kFloat ? AC_DTYPE_F32 : -1;
+    ac_view vq, vk{}, oq, ok{};
+    if (dtype < 0 || !rows(*q, type, dev, &vq)) return none();
+    const int64_t B = q->size(0), Hq = q->size(1), L = q->size(2), d = q->size(3), axes = i[2];
+    int64_t Hk = 0;
+    if (k) {
+        if (!rows(*k, type, dev, &vk)) return none();
+        Hk = k->size(1);
+        if (!same(*k, B, Hk, L, d)) return none();
     }
-    CATCH
+    if (!on(*pos, at::kInt, dev) || !pos->is_contiguous()) return none();
+    const bool per_sequence = pos->dim() == 3;
+    if (per_sequence ? pos->size(0) != B || pos->size(1) != L || pos->size(2) != axes
+                     : pos->dim() != 2 || pos->size(0) != L || pos->size(1) != axes)
+        return none();
+    if (!fits(B) || !fits(Hq) || !fits(Hk) || !fits(L) || !fits(d)) return none();
+    const Tensor yq = like(*q, {B, Hq, L, d}, type);
+    const Tensor yk = k ? like(*k, {B, Hk, L, d}, type) : Tensor();
+    oq = ac_view{yq.data_ptr(), Hq * L * d, L * d, d};
+    if (k) ok = ac_view{yk.data_ptr(), Hk * L * d, L * d, d};
+    const ac_status st = ac_rope_axes(dtype, &vq, &oq, (int32_t)Hq, &vk, &ok, (int32_t)Hk, (int32_t)B, (int32_t)L, (int32_t)d,
+                                      static_cast<const int32_t *>(pos->data_ptr()), per_sequence ? L * axes : 0,
+                                      reinterpret_cast<const double *>(i[0]), reinterpret_cast<const int32_t *>(i[1]),
+                                      (int32_t)axes, i[4] != 0, i[5] != 0, stream(dev));
+    if (st != AC_OK) return error(st);
+    return k ? two(yq, yk) : THPVariable_Wrap(yq);
+    END_HANDLE_TH_ERRORS
 }
 
 struct Window {
@@ -137,81 +131,79 @@ struct Window {
 
 // window(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, lse wanted)
 PyObject *window(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    try {
-        Window win;
-        if (n != 11 || !win.read(args + 3)) return none();
-        const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]);
-        if (!q || !k || !v || !q->is_cuda()) return none();
-        const c10::DeviceIndex dev = q->get_device();
-        ac_view vq, vk, vv;
-        if (dev != c10::cuda::current_device() || !rows(*q, at::kBFloat16, dev, &vq) || !rows(*k, at::kBFloat16, dev, &vk) ||
-            !rows(*v, at::kBFloat16, dev, &vv))
-            return none();
-        const int64_t B = q->size(0), Hq = q->size(1), Lq = q->size(2), d = q->size(3), Hk = k->size(1), Lk = k->size(2);
-        const int32_t *ql, *kl;
-        if (!same(*k, B, Hk, Lk, d) || !same(*v, B, Hk, Lk, d) || !lens(args[8], B, dev, &ql) || !lens(args[9], B, dev, &kl) ||
-            !fits(B) || !fits(Hq) || !fits(Hk) || !fits(Lq) || !fits(Lk) || !fits(d))
-            return none();
-        const bool want = args[10] == Py_True;
-        int64_t bytes = 0;
-        ac_status st = ac_window_attn_workspace((int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, &win.w, &bytes);
-        if (st != AC_OK) return error(st);
-        const Tensor o = like(*q, {B, Hq, Lq, d}, at::kBFloat16);
-        const Tensor lse = want ? like(*q, {B, Hq, Lq}, at::kFloat) : Tensor();
-        const Tensor ws = bytes ? like(*q, {bytes}, at::kByte) : Tensor();
-        const ac_view vo{o.data_ptr(), Hq * Lq * d, Lq * d, d};
-        st = ac_window_attn(&vq, &vk, &vv, &vo, want ? static_cast<float *>(lse.data_ptr()) : nullptr, (int32_t)B, (int32_t)Hq,
-                            (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, ql, kl, &win.w, bytes ? ws.data_ptr() : nullptr,
-                            bytes, stream(dev));
-        if (st != AC_OK) return error(st);
-        return want ? two(o, lse) : THPVariable_Wrap(o);
-    }
-    CATCH
+    HANDLE_TH_ERRORS
+    Window win;
+    if (n != 11 || !win.read(args + 3)) return none();
+    const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]);
+    if (!q || !k || !v || !q->is_cuda()) return none();
+    const c10::DeviceIndex dev = q->get_device();
+    ac_view vq, vk, vv;
+    if (dev != c10::cuda::current_device() || !rows(*q, at::kBFloat16, dev, &vq) || !rows(*k, at::kBFloat16, dev, &vk) ||
+        !rows(*v, at::kBFloat16, dev, &vv))
+        return none();
+    const int64_t B = q->size(0), Hq = q->size(1), Lq = q->size(2), d = q->size(3), Hk = k->size(1), Lk = k->size(2);
+    const int32_t *ql, *kl;
+    if (!same(*k, B, Hk, Lk, d) || !same(*v, B, Hk, Lk, d) || !lens(args[8], B, dev, &ql) || !lens(args[9], B, dev, &kl) ||
+        !fits(B) || !fits(Hq) || !fits(Hk) || !fits(Lq) || !fits(Lk) || !fits(d))
+        return none();
+    const bool want = args[10] == Py_True;
+    int64_t bytes = 0;
+    ac_status st = ac_window_attn_workspace((int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, &win.w, &bytes);
+    if (st != AC_OK) return error(st);
+    const Tensor o = like(*q, {B, Hq, Lq, d}, at::kBFloat16);
+    const Tensor lse = want ? like(*q, {B, Hq, Lq}, at::kFloat) : Tensor();
+    const Tensor ws = bytes ? like(*q, {bytes}, at::kByte) : Tensor();
+    const ac_view vo{o.data_ptr(), Hq * Lq * d, Lq * d, d};
+    st = ac_window_attn(&vq, &vk, &vv, &vo, want ? static_cast<float *>(lse.data_ptr()) : nullptr, (int32_t)B, (int32_t)Hq,
+                        (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, ql, kl, &win.w, bytes ? ws.data_ptr() : nullptr,
+                        bytes, stream(dev));
+    if (st != AC_OK) return error(st);
+    return want ? two(o, lse) : THPVariable_Wrap(o);
+    END_HANDLE_TH_ERRORS
 }
 
 // backward(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens)
 PyObject *backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    try {
-        Window win;
-        if (n != 13 || !win.read(args + 6)) return none();
-        const Tensor *t[6];
-        for (int i = 0; i < 6; ++i)
-            if (!(t[i] = tensor(args[i])) || !t[i]->is_cuda()) return none();
-        const c10::DeviceIndex dev = t[1]->get_device();
-        ac_view v[5];
-        if (dev != c10::cuda::current_device()) return none();
-        for (int i = 0; i < 5; ++i)
-            if (!rows(*t[i], at::kBFloat16, dev, &v[i])) return none();
-        const int64_t B = t[1]->size(0), Hq = t[1]->size(1), Lq = t[1]->size(2), d = t[1]->size(3);
-        const int64_t Hk = t[2]->size(1), Lk = t[2]->size(2);
-        const Tensor &lse = *t[5];
-        const int32_t *ql, *kl;
-        if (!same(*t[0], B, Hq, Lq, d) || !same(*t[4], B, Hq, Lq, d) || !same(*t[2], B, Hk, Lk, d) || !same(*t[3], B, Hk, Lk, d) ||
-            !on(lse, at::kFloat, dev) || lse.dim() != 3 || lse.size(0) != B || lse.size(1) != Hq || lse.size(2) != Lq ||
-            !lse.is_contiguous() || !lens(args[11], B, dev, &ql) || !lens(args[12], B, dev, &kl) || !fits(B) || !fits(Hq) ||
-            !fits(Hk) || !fits(Lq) || !fits(Lk) || !fits(d))
-            return none();
-        int64_t bytes = 0;
-        ac_status st = ac_window_attn_backward_workspace((int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d,
-                                                         &win.w, &bytes);
-        if (st != AC_OK) return error(st);
-        const Tensor dq = like(*t[1], {B, Hq, Lq, d}, at::kBFloat16), dk = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16),
-                     dv = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16);
-        const Tensor ws = bytes ? like(*t[1], {bytes}, at::kByte) : Tensor();
-        const ac_view vdq{dq.data_ptr(), Hq * Lq * d, Lq * d, d}, vdk{dk.data_ptr(), Hk * Lk * d, Lk * d, d},
-            vdv{dv.data_ptr(), Hk * Lk * d, Lk * d, d};
-        st = ac_window_attn_backward(&v[0], &v[1], &v[2], &v[3], &v[4], static_cast<const float *>(lse.data_ptr()), &vdq, &vdk, &vdv,
-                                     (int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, ql, kl, &win.w,
-                                     bytes ? ws.data_ptr() : nullptr, bytes, stream(dev));
-        if (st != AC_OK) return error(st);
-        PyObject *r = PyTuple_New(3);
-        if (!r) return nullptr;
-        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(dq));
-        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(dk));
-        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(dv));
-        return r;
-    }
-    CATCH
+    HANDLE_TH_ERRORS
+    Window win;
+    if (n != 13 || !win.read(args + 6)) return none();
+    const Tensor *t[6];
+    for (int i = 0; i < 6; ++i)
+        if (!(t[i] = tensor(args[i])) || !t[i]->is_cuda()) return none();
+    const c10::DeviceIndex dev = t[1]->get_device();
+    ac_view v[5];
+    if (dev != c10::cuda::current_device()) return none();
+    for (int i = 0; i < 5; ++i)
+        if (!rows(*t[i], at::kBFloat16, dev, &v[i])) return none();
+    const int64_t B = t[1]->size(0), Hq = t[1]->size(1), Lq = t[1]->size(2), d = t[1]->size(3);
+    const int64_t Hk = t[2]->size(1), Lk = t[2]->size(2);
+    const Tensor &lse = *t[5];
+    const int32_t *ql, *kl;
+    if (!same(*t[0], B, Hq, Lq, d) || !same(*t[4], B, Hq, Lq, d) || !same(*t[2], B, Hk, Lk, d) || !same(*t[3], B, Hk, Lk, d) ||
+        !on(lse, at::kFloat, dev) || lse.dim() != 3 || lse.size(0) != B || lse.size(1) != Hq || lse.size(2) != Lq ||
+        !lse.is_contiguous() || !lens(args[11], B, dev, &ql) || !lens(args[12], B, dev, &kl) || !fits(B) || !fits(Hq) ||
+        !fits(Hk) || !fits(Lq) || !fits(Lk) || !fits(d))
+        return none();
+    int64_t bytes = 0;
+    ac_status st = ac_window_attn_backward_workspace((int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d,
+                                                     &win.w, &bytes);
+    if (st != AC_OK) return error(st);
+    const Tensor dq = like(*t[1], {B, Hq, Lq, d}, at::kBFloat16), dk = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16),
+                 dv = like(*t[1], {B, Hk, Lk, d}, at::kBFloat16);
+    const Tensor ws = bytes ? like(*t[1], {bytes}, at::kByte) : Tensor();
+    const ac_view vdq{dq.data_ptr(), Hq * Lq * d, Lq * d, d}, vdk{dk.data_ptr(), Hk * Lk * d, Lk * d, d},
+        vdv{dv.data_ptr(), Hk * Lk * d, Lk * d, d};
+    st = ac_window_attn_backward(&v[0], &v[1], &v[2], &v[3], &v[4], static_cast<const float *>(lse.data_ptr()), &vdq, &vdk, &vdv,
+                                 (int32_t)B, (int32_t)Hq, (int32_t)Hk, (int32_t)Lq, (int32_t)Lk, (int32_t)d, ql, kl, &win.w,
+                                 bytes ? ws.data_ptr() : nullptr, bytes, stream(dev));
+    if (st != AC_OK) return error(st);
+    PyObject *r = PyTuple_New(3);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(dq));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(dk));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(dv));
+    return r;
+    END_HANDLE_TH_ERRORS
 }
 
 // The tensors of a cache: k, v, k_scale, v_scale.
@@ -242,60 +234,58 @@ bool table_of(PyObject *o, int64_t B, c10::DeviceIndex dev, const int32_t **p, i
 
 // append(k, v, cache's four tensors, page_table, start, counts): True when done
 PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    try {
-        if (n != 9) return none();
-        const Tensor *k = tensor(args[0]), *v = tensor(args[1]);
-        if (!k || !v || !k->is_cuda()) return none();
-        const c10::DeviceIndex dev = k->get_device();
-        ac_view vk, vv;
-        ac_cache8 c;
-        if (dev != c10::cuda::current_device() || !rows(*k, at::kBFloat16, dev, &vk) || !rows(*v, at::kBFloat16, dev, &vv) ||
-            !cache_of(args + 2, dev, &c))
-            return none();
-        const int64_t B = k->size(0), H = k->size(1), len = k->size(2), d = k->size(3);
-        const int32_t *table, *start, *counts;
-        int32_t per;
-        if (!same(*v, B, H, len, d) || H != c.heads || d != c.d || !fits(B) || !fits(len) || !table_of(args[6], B, dev, &table, &per) ||
-            args[7] == Py_None || !lens(args[7], B, dev, &start) || !lens(args[8], B, dev, &counts))
-            return none();
-        const ac_status st = ac_cache8_append(&c, &vk, &vv, (int32_t)B, (int32_t)len, table, per, start, counts, stream(dev));
-        if (st != AC_OK) return error(st);
-        Py_RETURN_TRUE;
-    }
-    CATCH
+    HANDLE_TH_ERRORS
+    if (n != 9) return none();
+    const Tensor *k = tensor(args[0]), *v = tensor(args[1]);
+    if (!k || !v || !k->is_cuda()) return none();
+    const c10::DeviceIndex dev = k->get_device();
+    ac_view vk, vv;
+    ac_cache8 c;
+    if (dev != c10::cuda::current_device() || !rows(*k, at::kBFloat16, dev, &vk) || !rows(*v, at::kBFloat16, dev, &vv) ||
+        !cache_of(args + 2, dev, &c))
+        return none();
+    const int64_t B = k->size(0), H = k->size(1), len = k->size(2), d = k->size(3);
+    const int32_t *table, *start, *counts;
+    int32_t per;
+    if (!same(*v, B, H, len, d) || H != c.heads || d != c.d || !fits(B) || !fits(len) || !table_of(args[6], B, dev, &table, &per) ||
+        args[7] == Py_None || !lens(args[7], B, dev, &start) || !lens(args[8], B, dev, &counts))
+        return none();
+    const ac_status st = ac_cache8_append(&c, &vk, &vv, (int32_t)B, (int32_t)len, table, per, start, counts, stream(dev));
+    if (st != AC_OK) return error(st);
+    Py_RETURN_TRUE;
+    END_HANDLE_TH_ERRORS
 }
 
 // cache_attn(q, cache's four tensors, page_table, k_lens, left, right, sinks, block, scale, q_lens, lse wanted)
 PyObject *cache_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    try {
-        Window win;
-        if (n != 14 || !win.read(args + 7)) return none();
-        const Tensor *q = tensor(args[0]);
-        if (!q || !q->is_cuda()) return none();
-        const c10::DeviceIndex dev = q->get_device();
-        ac_view vq;
-        ac_cache8 c;
-        if (dev != c10::cuda::current_device() || !rows(*q, at::kBFloat16, dev, &vq) || !cache_of(args + 1, dev, &c)) return none();
-        const int64_t B = q->size(0), Hq = q->size(1), Lq = q->size(2), d = q->size(3);
-        const int32_t *table, *ql, *kl;
-        int32_t per;
-        if (d != c.d || !fits(B) || !fits(Hq) || !fits(Lq) || !table_of(args[5], B, dev, &table, &per) || args[6] == Py_None ||
-            !lens(args[6], B, dev, &kl) || !lens(args[12], B, dev, &ql))
-            return none();
-        const bool want = args[13] == Py_True;
-        int64_t bytes = 0;
-        ac_status st = ac_cache8_attn_workspace(&c, (int32_t)B, (int32_t)Hq, (int32_t)Lq, per, &win.w, &bytes);
-        if (st != AC_OK) return error(st);
-        const Tensor o = like(*q, {B, Hq, Lq, d}, at::kBFloat16);
-        const Tensor lse = want ? like(*q, {B, Hq, Lq}, at::kFloat) : Tensor();
-        const Tensor ws = bytes ? like(*q, {bytes}, at::kByte) : Tensor();
-        const ac_view vo{o.data_ptr(), Hq * Lq * d, Lq * d, d};
-        st = ac_cache8_attn(&c, &vq, &vo, want ? static_cast<float *>(lse.data_ptr()) : nullptr, (int32_t)B, (int32_t)Hq, (int32_t)Lq,
-                            table, per, ql, kl, &win.w, bytes ? ws.data_ptr() : nullptr, bytes, stream(dev));
-        if (st != AC_OK) return error(st);
-        return want ? two(o, lse) : THPVariable_Wrap(o);
-    }
-    CATCH
+    HANDLE_TH_ERRORS
+    Window win;
+    if (n != 14 || !win.read(args + 7)) return none();
+    const Tensor *q = tensor(args[0]);
+    if (!q || !q->is_cuda()) return none();
+    const c10::DeviceIndex dev = q->get_device();
+    ac_view vq;
+    ac_cache8 c;
+    if (dev != c10::cuda::current_device() || !rows(*q, at::kBFloat16, dev, &vq) || !cache_of(args + 1, dev, &c)) return none();
+    const int64_t B = q->size(0), Hq = q->size(1), Lq = q->size(2), d = q->size(3);
+    const int32_t *table, *ql, *kl;
+    int32_t per;
+    if (d != c.d || !fits(B) || !fits(Hq) || !fits(Lq) || !table_of(args[5], B, dev, &table, &per) || args[6] == Py_None ||
+        !lens(args[6], B, dev, &kl) || !lens(args[12], B, dev, &ql))
+        return none();
+    const bool want = args[13] == Py_True;
+    int64_t bytes = 0;
+    ac_status st = ac_cache8_attn_workspace(&c, (int32_t)B, (int32_t)Hq, (int32_t)Lq, per, &win.w, &bytes);
+    if (st != AC_OK) return error(st);
+    const Tensor o = like(*q, {B, Hq, Lq, d}, at::kBFloat16);
+    const Tensor lse = want ? like(*q, {B, Hq, Lq}, at::kFloat) : Tensor();
+    const Tensor ws = bytes ? like(*q, {bytes}, at::kByte) : Tensor();
+    const ac_view vo{o.data_ptr(), Hq * Lq * d, Lq * d, d};
+    st = ac_cache8_attn(&c, &vq, &vo, want ? static_cast<float *>(lse.data_ptr()) : nullptr, (int32_t)B, (int32_t)Hq, (int32_t)Lq,
+                        table, per, ql, kl, &win.w, bytes ? ws.data_ptr() : nullptr, bytes, stream(dev));
+    if (st != AC_OK) return error(st);
+    return want ? two(o, lse) : THPVariable_Wrap(o);
+    END_HANDLE_TH_ERRORS
 }
 
 PyMethodDef methods[] = {
