@@ -8,7 +8,8 @@
 // rounded to 2^-64 once on the host, and pos * turns modulo 2^64 is exact for
 // every 32-bit position, so a position of a million loses nothing (in fp32 the
 // angle itself would be off by 2^-24 relative, 0.06 rad there).  sincospif
-// takes the top 32 bits.
+// takes the top 32 bits, rounded, as a float; the up to 7 bits that a float does not hold
+// turn its sine and cosine a little further, which leaves 2^-32 turns of error.
 //
 // Bound by memory: every element is read and written once.  A thread owns one
 // token and one 16-byte chunk (two chunks when the pair's halves lie d/2 apart),
@@ -69,8 +70,12 @@ struct Vec<__half> {
 
 __device__ __forceinline__ void pair_sincos(const RopeArgs &a, const int *pos, int p, float &s, float &c) {
     const uint64_t t = (uint64_t)(int64_t)pos[a.axis[p]] * a.turns[p];
-    const float half_turns = (float)(int32_t)(t >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-    sincospif(half_turns, &s, &c);
+    const int32_t units = (int32_t)((t + (1ull << 31)) >> 32);  // of 2^-31 half turns
+    const float f = __int2float_rz(units);  // (towards 0: within int32 again)
+    sincospif(f * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
+    const float rest = (float)(units - __float2int_rz(f)) * 1.4629180792671596e-9f;  // pi 2^-31
+    const float s0 = s;
+    s = fmaf(c, rest, s), c = fmaf(-s0, rest, c);
     if (a.inverse) s = -s;
 }
 

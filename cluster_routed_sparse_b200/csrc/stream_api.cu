@@ -92,8 +92,41 @@ cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     return few_rows(a) ? launch_window_few(a, s) : launch_window_mma(a, s);
 }
 
-// Turns per step modulo 1 of n frequencies, in units of 2^-64, to the nearest.  The last
-// frequencies' stay at hand: 0.5 us of a call of 8 us.
+// f / (2 pi) modulo 1 in units of 2^-64, to the nearest; 0 from |f| = 2^126 on.  f is a 53-bit
+// integer times a power of two, and 1 / (2 pi) is held to 192 bits, so whole turns leave
+// exactly and the fraction keeps all its bits.
+uint64_t turns_of(double f) {
+    constexpr uint64_t kInv[3] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull};  // of 2^-64, 2^-128, 2^-192
+    int x;
+    const double m = std::frexp(std::fabs(f), &x);
+    if (m == 0.0 || x < -62 || x > 126) return 0;
+    const uint64_t i = (uint64_t)std::ldexp(m, 53);
+    x -= 53;  // |f| = i 2^x
+    // i / (2 pi) modulo 2^64 in words: the whole turns, and three of the fraction
+    uint64_t w[4];
+    unsigned __int128 carry = 0;
+    for (int k = 2; k >= 0; --k) {
+        const unsigned __int128 p = (unsigned __int128)i * kInv[k] + carry;
+        w[k + 1] = (uint64_t)p;
+        carry = p >> 64;
+    }
+    w[0] = (uint64_t)carry;
+    // the 64 bits behind the point, once that has moved by x, and the bit after them
+    const int from = 64 + x;  // bit position in w, from its top
+    auto bit_word = [&](int at) -> uint64_t {  // 64 bits that begin at position `at`, zeros in front of w and behind it
+        uint64_t r = 0;
+        for (int k = 0; k < 4; ++k) {
+            const int d = at - 64 * k;
+            if (d >= 0 && d < 64) r |= w[k] << d;
+            else if (d < 0 && d > -64) r |= w[k] >> -d;
+        }
+        return r;
+    };
+    const uint64_t units = bit_word(from) + (bit_word(from + 64) >> 63);
+    return f < 0 ? 0 - units : units;
+}
+
+// The same of n frequencies.  The last ones' stay at hand: 0.5 us of a call of 8 us.
 bool turns_of(const double *freq, int n, uint64_t *turns) {
     thread_local double last[128];
     thread_local uint64_t last_turns[128];
@@ -102,10 +135,7 @@ bool turns_of(const double *freq, int n, uint64_t *turns) {
         last_n = -1;
         for (int k = 0; k < n; ++k) {
             if (!std::isfinite(freq[k])) return false;
-            long double t = (long double)freq[k] * 0.159154943091895335768883763372514362L;
-            if (t >= 1.0L || t <= -1.0L) t = fmodl(t, 1.0L);
-            const uint64_t units = (uint64_t)((t < 0 ? -t : t) * 18446744073709551615.0L + 0.5L);
-            last_turns[k] = t < 0 ? 0 - units : units;
+            last_turns[k] = turns_of(freq[k]);
             last[k] = freq[k];
         }
         last_n = n;

@@ -444,7 +444,8 @@ typedef enum ac_dtype { AC_DTYPE_BF16 = 0, AC_DTYPE_F16 = 1, AC_DTYPE_F32 = 2 } 
  * rotates back, which is also the gradient.  positions: device int32
  * [L, n_axes] for every sequence (pos_stride_b = 0) or per sequence
  * (pos_stride_b = entries from one to the next).  Angles are exact to 2^-32
- * turns at every position.  d even, at most 256; any strides (an output's not 0).
+ * turns at every position, for frequencies below 2^126 (from there on they count as 0);
+ * sine and cosine to an ulp and a half of fp32.  d even, at most 256; any strides (an output's not 0).
  * y may be x itself.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, d, device), CUDA. */
 AC_API ac_status ac_rope_axes(int32_t dtype, const ac_view *x, const ac_view *y, int32_t H, const ac_view *x2,
