@@ -662,7 +662,9 @@ Parts plan_parts(const WinArgs &a) {
     const int64_t all = query_tiles(a), tiles_k = (a.Lk + 127) / 128, heads = (int64_t)a.B * a.Hk;
     Parts pt{1 << 30, 1, 0};
     if (all == 0 || tiles_k == 0) return pt;
-    const int64_t window = std::min(all, window_tiles(a.w, 128, a.Lk, a.Lq, 128 / a.G));  // of keys without the first tokens
+    WinRule w = a.w;
+    w.sinks = 0;  // (a key that is no first token is seen by its window alone)
+    const int64_t window = std::min(all, window_tiles(w, 128, a.Lk, a.Lq, 128 / a.G));  // of keys without the first tokens
     const int64_t first = a.w.left < 0 ? tiles_k : std::min<int64_t>(tiles_k, (a.w.sinks + (int64_t)127) / 128);
     const int64_t total = a.w.left < 0 ? heads * tiles_k * (a.w.right < 0 ? all : (all + 1) / 2)
                                        : heads * (first * all + (tiles_k - first) * window);
