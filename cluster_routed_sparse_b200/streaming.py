@@ -24,19 +24,31 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import numbers
 import operator
+import os
+import warnings
 from typing import NamedTuple
 
 import torch
 
 from . import _lib
 from ._lib import ACCache8, ACView, ACWindow, check
+from .build import FAST
 
-try:
-    from . import _fast
-except ImportError:  # built with libac.so; without it every call takes the way below
-    _fast = None
+
+def _load_fast():
+    """The compiled module, or None: every call then takes the way through ctypes."""
+    try:
+        return importlib.import_module("._fast", __package__)
+    except ImportError as e:
+        if os.path.exists(FAST):
+            warnings.warn(f"{FAST} does not load, calls go through ctypes (build again?): {e}", RuntimeWarning)
+        return None
+
+
+_fast = _load_fast()
 
 _ROPE_DTYPES = {torch.bfloat16: _lib.AC_DTYPE_BF16, torch.float16: _lib.AC_DTYPE_F16, torch.float32: _lib.AC_DTYPE_F32}
 _NO_VIEW = ACView(None, 0, 0, 0)
