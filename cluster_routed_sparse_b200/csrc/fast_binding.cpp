@@ -4,11 +4,12 @@
 //
 // Each function here takes the common case (tensors on the current CUDA device
 // with the right types and shapes, new outputs) through the C ABI of libac; for
-// everything else, wrong arguments included, it returns None, and the caller in
-// streaming.py goes its own way, which checks and explains.
+// everything else, wrong arguments and tensors that autograd records included, it returns
+// None, and the caller in streaming.py goes its own way, which checks and explains.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -66,6 +67,11 @@ Tensor like(const Tensor &t, at::IntArrayRef shape, at::ScalarType type) {
     return at::empty(shape, t.options().dtype(type));
 }
 
+// Whether autograd records what is done with the tensor: backwards, or its tangent forwards.
+bool recorded(const Tensor &t) {
+    return (at::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(0).defined();
+}
+
 void *stream(c10::DeviceIndex dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
 PyObject *none() { Py_RETURN_NONE; }
@@ -86,7 +92,7 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
     int64_t i[6];
     if (n != 9 || !integers(args + 3, 6, i)) return none();
     const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *pos = tensor(args[2]);
-    if (!q || !pos || !q->is_cuda() || (!k && args[1] != Py_None)) return none();
+    if (!q || !pos || !q->is_cuda() || (!k && args[1] != Py_None) || recorded(*q) || (k && recorded(*k))) return none();
     const c10::DeviceIndex dev = q->get_device();
     if (dev != c10::cuda::current_device()) return none();
     const at::ScalarType type = q->scalar_type();
@@ -135,7 +141,7 @@ PyObject *window(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Window win;
     if (n != 11 || !win.read(args + 3)) return none();
     const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]);
-    if (!q || !k || !v || !q->is_cuda()) return none();
+    if (!q || !k || !v || !q->is_cuda() || recorded(*q) || recorded(*k) || recorded(*v)) return none();
     const c10::DeviceIndex dev = q->get_device();
     ac_view vq, vk, vv;
     if (dev != c10::cuda::current_device() || !rows(*q, at::kBFloat16, dev, &vq) || !rows(*k, at::kBFloat16, dev, &vk) ||
@@ -169,7 +175,7 @@ PyObject *backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 13 || !win.read(args + 6)) return none();
     const Tensor *t[6];
     for (int i = 0; i < 6; ++i)
-        if (!(t[i] = tensor(args[i])) || !t[i]->is_cuda()) return none();
+        if (!(t[i] = tensor(args[i])) || !t[i]->is_cuda() || recorded(*t[i])) return none();
     const c10::DeviceIndex dev = t[1]->get_device();
     ac_view v[5];
     if (dev != c10::cuda::current_device()) return none();
@@ -237,7 +243,7 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (n != 9) return none();
     const Tensor *k = tensor(args[0]), *v = tensor(args[1]);
-    if (!k || !v || !k->is_cuda()) return none();
+    if (!k || !v || !k->is_cuda() || recorded(*k) || recorded(*v)) return none();
     const c10::DeviceIndex dev = k->get_device();
     ac_view vk, vv;
     ac_cache8 c;
@@ -262,7 +268,7 @@ PyObject *cache_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Window win;
     if (n != 14 || !win.read(args + 7)) return none();
     const Tensor *q = tensor(args[0]);
-    if (!q || !q->is_cuda()) return none();
+    if (!q || !q->is_cuda() || recorded(*q)) return none();
     const c10::DeviceIndex dev = q->get_device();
     ac_view vq;
     ac_cache8 c;

@@ -13,8 +13,13 @@ video generator that works frame after frame.
 Each call forwards data pointers, strides and the current stream of the
 tensors' device to the C ABI in include/ac.h, which documents the operators;
 all arithmetic runs in libac's kernels.  Tensors are [B, H, L, d] in any strides
-(d contiguous).  Nothing here synchronises but ops_status, and nothing is
-recorded by autograd: gradients are calls of their own.
+(d contiguous).  Nothing here synchronises but ops_status.
+
+Gradients are calls of their own (rope_axes(inverse=True), window_attn_backward),
+and rope_axes and window_attn make them where autograd records: for tensors that
+require gradients, with new outputs.  window_attn has no second derivative and none
+of its lse.  What is not recorded (outputs written into given tensors, the cache,
+window_attn_backward itself) warns when one of its inputs requires gradients.
 
 The common case of a call (new outputs, tensors on the current device) goes
 through the compiled _fast module, which makes the same C calls; what it does
@@ -32,6 +37,8 @@ import warnings
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import ACCache8, ACView, ACWindow, check
@@ -76,6 +83,70 @@ def _on(device, fn, *args):
             status = fn(*args, _raw_stream(device.index))
     if status:
         check(status)
+
+
+# ---------------------------------------------------------------- autograd
+def _recorded(*tensors):
+    """Whether autograd records what is done with one of them: backwards, or its tangent forwards."""
+    tensors = [t for t in tensors if t is not None]
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors) or \
+        forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def _warn_if_recorded(what, *tensors):
+    if _recorded(*tensors):
+        warnings.warn(f"{what} is not recorded by autograd: its result carries no gradients", UserWarning, stacklevel=3)
+
+
+def _rows16(t):
+    """t in strides that the attention takes (gradients come in any: broadcast, transposed)."""
+    fits = t.data_ptr() % 16 == 0 and t.stride(3) == 1 and \
+        all(n <= 1 or s > 0 and s % 8 == 0 for n, s in zip(t.shape[:3], t.stride()[:3]))
+    return t if fits else t.clone(memory_format=torch.contiguous_format)
+
+
+class _RopeAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inverse, args):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.inverse, ctx.args = inverse, args
+        return _rope_now(q, k, positions, *args, inverse)
+
+    @staticmethod
+    def backward(ctx, gq, gk=None):
+        positions, = ctx.saved_tensors
+        grads = [g if n else None for g, n in zip((gq, gk), ctx.needs_input_grad)]
+        given = [g if g.stride(3) == 1 else g.contiguous() for g in grads if g is not None]
+        if not given:
+            return None, None, None, None, None
+        if _recorded(*given):  # (a rotation too)
+            r = _RopeAxes.apply(given[0], given[1] if len(given) > 1 else None, positions, not ctx.inverse, ctx.args)
+        else:
+            r = _rope_now(given[0], given[1] if len(given) > 1 else None, positions, *ctx.args, not ctx.inverse)
+        r = list(r) if len(given) > 1 else [r]
+        return *(None if g is None else r.pop(0) for g in grads), None, None, None
+
+
+class _WindowAttn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_lens, k_lens, rule, return_lse):
+        ctx.set_materialize_grads(False)
+        o, lse = _window_now(q, k, v, *rule, q_lens, k_lens, True)
+        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
+        ctx.rule = rule
+        return (o, lse) if return_lse else o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g, g_lse=None):
+        if g_lse is not None:
+            raise RuntimeError("window_attn: lse has no gradient")
+        if g is None:
+            return (None,) * 7
+        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        grads = _backward_now(_rows16(g), q, k, v, o, lse, *ctx.rule, q_lens, k_lens)
+        return *(x if n else None for x, n in zip(grads, ctx.needs_input_grad)), None, None, None, None
 
 
 def _shape(t, name):
@@ -165,10 +236,30 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
             freq, npairs, pf, pn = _axes_given(pairs, tuple(map(float, freqs)))
         else:
             freq, npairs, pf, pn = _axes(pairs, tuple(map(float, theta)) if isinstance(theta, (list, tuple)) else float(theta))
-    if _fast is not None and out is None:
-        r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), 1 if interleaved else 0, 1 if inverse else 0)
+    args = (npairs, pf, pn, axes, freq, 1 if interleaved else 0)
+    inverse = 1 if inverse else 0
+    if out is None:
+        if _fast is not None:
+            r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), args[5], inverse)
+            if _took(r):
+                return r
+        if _recorded(q, k):
+            return _RopeAxes.apply(q, k, positions, inverse, args)
+    else:
+        _warn_if_recorded("rope_axes(out=...)", q, k)
+    return _rope_ctypes(q, k, positions, *args, inverse, out)
+
+
+def _rope_now(q, k, positions, npairs, pf, pn, axes, freq, interleaved, inverse):
+    """New outputs, whatever autograd thinks of the inputs."""
+    if _fast is not None:
+        r = _fast.rope(q, k, positions, pf, pn, axes, len(freq), interleaved, 1 if inverse else 0)
         if _took(r):
             return r
+    return _rope_ctypes(q, k, positions, npairs, pf, pn, axes, freq, interleaved, inverse, None)
+
+
+def _rope_ctypes(q, k, positions, npairs, pf, pn, axes, freq, interleaved, inverse, out):
     dt = q.dtype
     dtype = _ROPE_DTYPES.get(dt)
     if dtype is None:
@@ -194,7 +285,7 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
             ok = q.new_empty(kshape)
         vko = _view(ok, "out[1]", dev, kshape, dt)
     _on(dev, _lib.load().ac_rope_axes, dtype, vq, vqo, Hq, vk, vko, Hk, B, L, d, pos, pos_b, freq, npairs, axes,
-        1 if interleaved else 0, 1 if inverse else 0)
+        interleaved, 1 if inverse else 0)
     return oq if k is None else (oq, ok)
 
 
@@ -236,10 +327,29 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
     `block` tokens, plus the first `sinks` tokens (ac_window_attn; struct
     ac_window says exactly which keys a query sees).  q_lens, k_lens: int32 [B]
     lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32."""
-    if _fast is not None and out is None:
-        r = _fast.window(q, k, v, left, right, sinks, block, float(scale), q_lens, k_lens, bool(return_lse))
+    scale = float(scale)
+    if out is None:
+        if _fast is not None:
+            r = _fast.window(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, bool(return_lse))
+            if _took(r):
+                return r
+        if _recorded(q, k, v):
+            return _WindowAttn.apply(q, k, v, q_lens, k_lens, (left, right, sinks, block, scale), bool(return_lse))
+    else:
+        _warn_if_recorded("window_attn(out=...)", q, k, v)
+    return _window_ctypes(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, return_lse, out)
+
+
+def _window_now(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, return_lse):
+    """New outputs, whatever autograd thinks of the inputs."""
+    if _fast is not None:
+        r = _fast.window(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, return_lse)
         if _took(r):
             return r
+    return _window_ctypes(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, return_lse, None)
+
+
+def _window_ctypes(q, k, v, left, right, sinks, block, scale, q_lens, k_lens, return_lse, out):
     dev = q.device
     shape = _shape(q, "q")
     B, Hq, Lq, d = shape
@@ -271,10 +381,25 @@ def window_attn_backward(d_out, q, k, v, o, lse, *, left: int = -1, right: int =
     """Gradients (dq, dk, dv) of window_attn with the same window and lengths, from
     d_out, the gradient of o, and the o and lse that it returned
     (ac_window_attn_backward).  out: (dq, dk, dv) to write into."""
+    scale = float(scale)
     if _fast is not None and out is None:
-        r = _fast.backward(d_out, q, k, v, o, lse, left, right, sinks, block, float(scale), q_lens, k_lens)
+        r = _fast.backward(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens)
         if _took(r):
             return r
+    _warn_if_recorded("window_attn_backward", d_out, q, k, v, o, lse)
+    return _backward_ctypes(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens, out)
+
+
+def _backward_now(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens):
+    """New outputs, whatever autograd thinks of the inputs."""
+    if _fast is not None:
+        r = _fast.backward(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens)
+        if _took(r):
+            return r
+    return _backward_ctypes(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens, None)
+
+
+def _backward_ctypes(d_out, q, k, v, o, lse, left, right, sinks, block, scale, q_lens, k_lens, out):
     dev = q.device
     qs = _shape(q, "q")
     B, Hq, Lq, d = qs
@@ -333,6 +458,7 @@ def cache8_append(k, v, cache: Cache8, page_table, start, counts=None):
     [B, max_pages]; start, counts: int32 [B] (counts: how many of the n are real)."""
     if _fast is not None and _took(_fast.append(k, v, *cache, page_table, start, counts)):
         return
+    _warn_if_recorded("cache8_append", k, v)
     dev = k.device
     shape = _shape(k, "k")
     B, H, n, d = shape
@@ -365,6 +491,7 @@ def cache8_attn(q, cache: Cache8, page_table, k_lens, *, left: int = -1, right: 
         r = _fast.cache_attn(q, *cache, page_table, k_lens, left, right, sinks, block, float(scale), q_lens, bool(return_lse))
         if _took(r):
             return r
+    _warn_if_recorded("cache8_attn", q)
     dev = q.device
     shape = _shape(q, "q")
     vq = _view(q, "q", dev, shape)
