@@ -778,7 +778,18 @@ ac_status ac_create(const ac_config *cfg, int32_t B, int32_t H, int32_t L, int32
         cudaMemset(c->Vp, 0, BH * (size_t)c->Lpad * dz * sizeof(bf16)) != cudaSuccess ||
         // an empty cluster's member mean is never written: keep it finite
         (c->kbar && cudaMemset(c->kbar, 0, BH * Cc * dz * sizeof(float)) != cudaSuccess) ||
-        (c->vbar && cudaMemset(c->vbar, 0, BH * Cc * dz * sizeof(float)) != cudaSuccess)) {
+        (c->vbar && cudaMemset(c->vbar, 0, BH * Cc * dz * sizeof(float)) != cudaSuccess) ||
+        // what lies behind the last cluster, and behind the selected ones, can be viewed and exported:
+        // zeros, not what was in the memory before
+        cudaMemset(c->cent_k, 0, BH * Cc * dz * sizeof(*c->cent_k)) != cudaSuccess ||
+        cudaMemset(c->counts_k, 0, BH * Cc * sizeof(*c->counts_k)) != cudaSuccess ||
+        cudaMemset(c->kmax, 0, BH * Cc * dz * sizeof(*c->kmax)) != cudaSuccess ||
+        cudaMemset(c->kmin, 0, BH * Cc * dz * sizeof(*c->kmin)) != cudaSuccess ||
+        cudaMemset(c->sse, 0, BH * Cc * sizeof(*c->sse)) != cudaSuccess ||
+        cudaMemset(c->score, 0, BH * Cq * Cc * sizeof(*c->score)) != cudaSuccess ||
+        cudaMemset(c->sel, 0, BH * Cq * Cc * sizeof(*c->sel)) != cudaSuccess ||
+        // (the caller's streams need not wait for the default one)
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
         free_all(c);
         delete c;
         return AC_ERR_CUDA;
