@@ -90,7 +90,7 @@ def _recorded(*tensors):
     """Whether autograd records what is done with one of them: backwards, or its tangent forwards."""
     tensors = [t for t in tensors if t is not None]
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors) or \
-        forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+        getattr(forward_ad, "_current_level", -1) >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _warn_if_recorded(what, *tensors):
