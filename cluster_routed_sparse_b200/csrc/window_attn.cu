@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(Split<C8>::THREADS, 1) k_window_attn(const __g
 
     const uint32_t bar0 = sbase + LY::OFF_BAR;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_or_note(bar, parity, &p.err->timeout, p.launch); };
+    // (a local pointer: with the expression in the call the compiler spills more)
+    uint32_t *noted = &p.err->timeout;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_or_note(bar, parity, noted, p.launch); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + LY::OFF_BAR + 8 * NBAR);
 
     // K and V tiles j of the producer thread
