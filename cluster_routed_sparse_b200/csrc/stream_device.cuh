@@ -163,12 +163,12 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     const uint32_t h = e4m3x2_to_half2(two);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-// Two codes, times a power of two, as bf16.  Exact: a code has 4 significant bits and bf16
-// the exponents of fp32, so the upper halves of the two fp32 values are the result (a byte
-// permutation: twice the rate of a conversion).
+// Two codes, times their scale, as bf16.  Exact for a power of two: a code has 4 significant
+// bits, and bf16 has the exponents of fp32.  (Other scales round to nearest: taking the upper
+// halves of the fp32 values, which is no faster, would cut them off.)
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale = 1.f) {
     const float2 f = e4m3x2_to_float2(two);
-    return __byte_perm(__float_as_uint(f.x * scale), __float_as_uint(f.y * scale), 0x7632);
+    return pack_bf16x2(f.x * scale, f.y * scale);
 }
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }

@@ -94,3 +94,28 @@ def test_pages_of_small_values(Lq, n, H):
     # whose smallest step is 2^-133; half of it, times a code of 448 at most, for each key
     r["tol"]["o"] = r["tol"]["o"] - 1e-30 + n * 2.0 ** -125
     ref.check("o", o, r)
+
+
+@pytest.mark.parametrize("Lq,n,H", ROUTES)
+def test_scales_that_are_no_powers_of_two(Lq, n, H):
+    """A cache filled elsewhere may have any scales: the code times the scale then rounds to nearest, once, in bf16."""
+    T, d = 16, 64
+    g = gen(13)
+    c = random_cache(g, -(-n // T), H, T, d)
+    for s in (c.k_scale, c.v_scale):
+        s.copy_((torch.rand(s.shape, generator=g, device="cuda") + 1.0) * 2.0 ** -7)
+    c.v.copy_(c.v.float().abs())  # no sign to hide a bias in
+    table = torch.arange(c.k.shape[0], device="cuda", dtype=torch.int32).view(1, -1)
+    q = torch.randn(1, H, Lq, d, generator=g, device="cuda").to(torch.bfloat16)
+    o = crs.cache8_attn(q, c, table, torch.tensor([n], device="cuda", dtype=torch.int32), right=-1)
+    crs.ops_status()
+    # (the plain form on the products in fp32: dense() and its reader keep them)
+    k, v = dense(c, table, n)
+    s = (q.double() @ k.double().transpose(2, 3)) / 8.0
+    p = torch.softmax(s, 3)
+    want = p @ v.double()
+    # a key off by half a step of bf16 in each element moves its score by 2^-9 |q| |k| at most, and the weight as much
+    # again; random over 64 elements, an eighth of it: the norms tell a bias (2^-9 and more, of one sign) from that
+    off = (o.double() - want)
+    assert abs(float(off.sum() / want.sum())) < 2.0 ** -10
+    assert float(off.norm() / want.norm()) < 2.0 ** -6
