@@ -49,12 +49,12 @@ def _fast_stale() -> bool:
 def _build_fast(force: bool = False) -> None:
     """fast_binding.cpp against torch's headers, linked to libac.so beside it.  Where that cannot be done (no headers,
     no compiler) the package goes without it: streaming.py makes the same calls from Python."""
-    if not force and not _fast_stale():
-        return
-    for path in (FAST, STAMP):  # one built for another torch must not be found
-        if os.path.exists(path):
-            os.remove(path)
     try:
+        if not force and not _fast_stale():
+            return
+        for path in (FAST, STAMP):  # one built for another torch must not be found
+            if os.path.exists(path):
+                os.remove(path)
         import sysconfig
 
         import torch

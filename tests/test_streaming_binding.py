@@ -58,3 +58,10 @@ def test_one_that_does_not_load_is_named(monkeypatch, tmp_path):
     open(streaming.FAST, "w").close()
     with pytest.warns(RuntimeWarning, match="does not load"):
         assert streaming._load_fast() is None
+
+
+def test_without_torch_the_library_is_built(elsewhere, monkeypatch, capfd):
+    import sys
+    monkeypatch.setitem(sys.modules, "torch", None)  # importing it fails
+    build._build_fast()
+    assert not elsewhere and "ctypes" in capfd.readouterr().err
