@@ -12,7 +12,7 @@
 // shared heads add up in the accumulator.
 //
 // The row sum delta0 = sum dO o that the first role starts from uses o as the
-// forward rounded it, off by 2^-9 |dO| |o|: over thousands of keys that error,
+// forward rounded it, off by 2^-8 |dO| |o| at most: over thousands of keys that error,
 // times sum_j P_j k_j, would be the largest in dQ (1.2e-2 of its norm measured over
 // 5,000 keys, against 2e-3 from all other roundings).  Since sum_j dS_j = 0 for the
 // true delta, r = sum_j dS_j tells the error, and dQ = s (A2 - r A1) takes it
@@ -36,8 +36,9 @@
 // window_attn.cu: one column interval per thread.
 //
 // Bound by the tensor core and the hand-offs: 8 products of 128 x 128 x d per tile and
-// role pair, 3 more than one role with atomic sums into dQ would take, which is the
-// price of the same bits every time.  32,760 queries in frames of 1,560 over three
+// role pair where 5 are the gradient's own: S and dP are formed twice because each output
+// row has one owner (dQ summed across key tiles, by atomics or in turns, would save them), and
+// A1 = P K only takes the rounding of o out again.  32,760 queries in frames of 1,560 over three
 // frames and the first, 12 heads, d = 128: 4.66 TFLOP in 3.8 ms, 1.22 PFLOP/s, 72% of
 // the measured cuBLAS rate; 2,830 cycles a tile in the first role and 3,000 in the
 // second where the products take 2,048 (the scores' wait 500, P 1,380, of which the

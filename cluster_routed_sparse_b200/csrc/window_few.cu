@@ -62,7 +62,7 @@ struct FewParams {
     float *part_o, *part_lse;
 };
 
-// N 16-byte words (8 bytes for N = 0) from global memory, read once.
+// BYTES bytes (8, or a multiple of 16) from global memory, read once; zeros where not live.
 template <int BYTES>
 __device__ __forceinline__ void load_bytes(uint32_t (&r)[BYTES / 4], const void *src, bool live) {
     if constexpr (BYTES == 8) {

@@ -220,9 +220,10 @@ def rope_axes(q, k, positions, pairs, theta=10000.0, *, freqs=None, interleaved:
     theta: base of the frequencies, one or one for each axis, or freqs: radians
     per step of each pair.  interleaved: pairs (2p, 2p + 1), otherwise
     (p, P + p).  inverse=True rotates back: the gradient with respect to the
-    input is rope_axes(grad, ..., inverse=True).  out: (q, k) to write into,
-    the inputs themselves allowed; contiguous new tensors otherwise.  bf16, fp16 or
-    fp32.  Returns (q, k) rotated, or q alone when k is None."""
+    input is rope_axes(grad, ..., inverse=True), which autograd calls for new
+    outputs.  out: (q, k) to write into, the inputs themselves allowed;
+    contiguous new tensors otherwise.  bf16, fp16 or fp32.  Returns (q, k)
+    rotated, or q alone when k is None."""
     pairs = tuple(pairs)
     axes = len(pairs)
     try:
@@ -326,7 +327,8 @@ def window_attn(q, k, v, *, left: int = -1, right: int = 0, sinks: int = 0, bloc
     window of `left` blocks back and `right` ahead (-1: no bound), blocks of
     `block` tokens, plus the first `sinks` tokens (ac_window_attn; struct
     ac_window says exactly which keys a query sees).  q_lens, k_lens: int32 [B]
-    lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32."""
+    lengths of a padded batch.  Returns o, or (o, lse) with lse [B, Hq, Lq] fp32.
+    Gradients of o pass through a new output (window_attn_backward); lse has none."""
     scale = float(scale)
     if out is None:
         if _fast is not None:
