@@ -16,7 +16,7 @@
 //
 // One token of four sequences over 16,384 of 32,760 bf16 keys and 128 first ones, 40
 // heads (1.35 GB): 209 us in a graph, the rate of a copy.  One token of eight sequences
-// over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 106 us, 5.1 TB/s, 79% of it:
+// over 32,760 cached tokens, 8 key heads for 40 (0.54 GB): 108 us, 5.0 TB/s, 77% of it:
 // a warp waits for its loads and then works, and converting V to bf16 takes 8 us of that,
 // the second part of the weights 3 (fp16 codes and weights took 95, and lost weights;
 // integer steps instead of the two conversions 116; 5 CTAs on an SM spill, 152).
@@ -24,8 +24,10 @@
 // a cache of that size, 281 for 24.
 //
 // Over the 8-bit cache K enters its product as fp16 codes (one conversion for two of them), with
-// the scale of its page taken into the scores and Q divided by a power of two per row to fit
-// (elements below 2^-14 of the row's largest are off by 2^-25 of it), and V as bf16 codes.
+// the scale of its page taken into the scores and Q divided by a power of two per row to fit:
+// fp16 then holds its elements down to 2^-31 of the row's largest exactly.  Where one is
+// smaller, the CTA takes K as bf16 codes and Q as it is (three conversions more; the branch
+// costs 1 us of 107, a loop of its own for each 6).  V: bf16 codes.
 // Rounding: a weight is a sum of two bf16 values, hence off by 2^-17 at most, over
 // fp32's whole range of exponents; over the cache it takes the scale of V's page first, a power of
 // two, and the sum of the weights does without.  (In fp16 small weights lost their bits
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
 
     // ---- Q^T as the B operand: k16 step s holds elements t4 D/4 + 4 s + {0..3} of row g8
     uint32_t bq[KS][2];
+    bool wide = false;          // over the cache: Q stays bf16
     float g_c = fp.scale_log2;  // scale log2(e), times the power of two taken out of that row
     {
         uint32_t w[D / 8];
@@ -128,11 +131,17 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
             for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const int ex = top ? min(max((int)(top >> 7) - 127, -120), 120) : 0;  // |q| < 2^(ex + 1)
-            g_c *= exp2i(ex);
-            const float dn = exp2i(-ex);
+            const int ex = (top ? min(max((int)(top >> 7) - 127, -112), 120) : 0) - 14;  // |q| < 2^(ex + 15)
+            uint32_t least = 0xFFFFu;  // the smallest that is not 0 (0 - 1 is the largest)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
+            for (int i = 0; i < D / 8; ++i) least = min(least, min(((w[i] & 0x7FFFu) - 1u) & 0xFFFFu, (((w[i] >> 16) & 0x7FFFu) - 1u) & 0xFFFFu));
+            wide = __any_sync(0xFFFFFFFFu, (int)((least + 1u) >> 7) - 127 < ex - 17) != 0;
+            if (!wide) {
+                g_c *= exp2i(ex);
+                const float dn = exp2i(-ex);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) w[i] = pack_half2(__uint_as_float(w[i] << 16) * dn, __uint_as_float(w[i] & 0xFFFF0000u) * dn);
+            }
         }
 #pragma unroll
         for (int s = 0; s < KS; ++s) bq[s][0] = w[2 * s], bq[s][1] = w[2 * s + 1];
@@ -217,19 +226,28 @@ __global__ void __launch_bounds__(kThreads, C8 ? 4 : 3) k_window_few(const __gri
 
         // S^T: s[2 u + e] is key g8 + 8 u, row 2 t4 + e
         float s[4] = {};
+        if (C8 && wide) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            uint32_t a[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if constexpr (C8) {
-                    const uint32_t w = kw[u][k];  // 4 codes: one k16 step's share
-                    a[u] = e4m3x2_to_half2(w & 0xFFFFu), a[2 + u] = e4m3x2_to_half2(w >> 16);
-                } else {
-                    a[u] = kw[u][2 * k], a[2 + u] = kw[u][2 * k + 1];
-                }
+            for (int k = 0; k < KS; ++k) {
+                const uint32_t x = kw[0][k], y = kw[1][k];  // 4 codes: one k16 step's share
+                mma<false>(s, e4m3x2_to_bf16x2(x & 0xFFFFu), e4m3x2_to_bf16x2(y & 0xFFFFu), e4m3x2_to_bf16x2(x >> 16),
+                           e4m3x2_to_bf16x2(y >> 16), bq[k][0], bq[k][1]);
             }
-            mma<C8>(s, a[0], a[1], a[2], a[3], bq[k][0], bq[k][1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t a[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if constexpr (C8) {
+                        const uint32_t w = kw[u][k];
+                        a[u] = e4m3x2_to_half2(w & 0xFFFFu), a[2 + u] = e4m3x2_to_half2(w >> 16);
+                    } else {
+                        a[u] = kw[u][2 * k], a[2 + u] = kw[u][2 * k + 1];
+                    }
+                }
+                mma<C8>(s, a[0], a[1], a[2], a[3], bq[k][0], bq[k][1]);
+            }
         }
         if (more) load_k(nxt, base2);
 

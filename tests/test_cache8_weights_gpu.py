@@ -119,3 +119,26 @@ def test_scales_that_are_no_powers_of_two(Lq, n, H):
     off = (o.double() - want)
     assert abs(float(off.sum() / want.sum())) < 2.0 ** -10
     assert float(off.norm() / want.norm()) < 2.0 ** -6
+
+
+@pytest.mark.parametrize("Lq,n,H", ROUTES)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 100])
+def test_queries_with_one_large_channel(Lq, n, H, size):
+    """A channel of the queries `size` times the others, of which the keys hold nothing: the scores are the others'."""
+    T, d = 16, 64
+    g = gen(19)
+    c = random_cache(g, -(-n // T), H, T, d)
+    x = c.k.float()
+    x[..., 0] = 0
+    c.k.copy_(x)
+    table = torch.arange(c.k.shape[0], device="cuda", dtype=torch.int32).view(1, -1)
+    q = torch.randn(1, H, Lq, d, generator=g, device="cuda").to(torch.bfloat16)
+    q[..., 0] = size
+    if Lq > 1:
+        q[:, :, 1::3, 0] = 0  # (and rows without it)
+    o, lse = crs.cache8_attn(q, c, table, torch.tensor([n], device="cuda", dtype=torch.int32), right=-1, return_lse=True)
+    crs.ops_status()
+    k, v = dense(c, table, n)
+    r = ref.attention(q, k, v, ref.visible(1, Lq, n, -1, -1, 0, 1))
+    ref.check("o", o, r)
+    ref.check("lse", lse, r)
