@@ -40,8 +40,8 @@
 // Bound by the softmax's chain: a pair of row tiles takes 3,500 cycles per key tile (S
 // 1,100 waited for, its load 150, maximum 320, exponentials 1,310, P 285, per row tile)
 // where the products take 2,048.  Frame-causal, 32,760 tokens in frames of 1,560, three
-// frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,020 us alone, 1.14 PFLOP/s, 68%
-// of the measured cuBLAS rate; 1,190 us in a long loop under the power limit.  1,560
+// frames and the first, 12 heads, d = 128 (1.17 TFLOP): 1,040 us alone, 1.12 PFLOP/s, 67%
+// of the measured cuBLAS rate; 1,200 us in a long loop under the power limit.  1,560
 // rows over 18,720 keys, 12 heads (0.18 TFLOP): 204 us; over the codes of the 8-bit cache
 // 252, because every CTA converts them anew and reads its scores twice (registers go to
 // the converting threads): many rows take the cache as bf16 rows instead.  Dropped, in us
